@@ -10,6 +10,9 @@ device and the built library and raise otherwise.
 Names follow the layer: ``route`` (Cartesian Product Router), ``schedule``
 (Expert-Centric Scheduling), ``expert_forward`` (grouped execution),
 ``moe_forward`` (all three), ``token_centric_forward`` (the ablation).
+``grouped_linear`` and its backward run experts of any width from a schedule
+with one expert per group; ``quantize_rows`` and ``quantized_linear`` are the
+8-bit products.
 """
 from __future__ import annotations
 
@@ -20,14 +23,15 @@ import torch
 
 from . import _lib
 from ._lib import (OMNI_BF16, OMNI_F32, OMNI_FLAG_DENSE_TENSOR_CORES, OMNI_FLAG_ROUTER_SIMT,
-                   OMNI_FLAG_STAGED_SMALL,
+                   OMNI_FLAG_STAGED_SMALL, OMNI_LINEAR_SILU,
                    OMNI_WS_BACKWARD, OMNI_WS_EXPERT, OMNI_WS_FUSED,
                    OMNI_WS_ROUTE, OMNI_WS_SCHEDULE, OmniError)
 
 __all__ = ["LayerDims", "route", "router_logits", "route_select", "schedule", "expert_forward", "moe_forward",
            "token_centric_forward", "new_counts", "OmniError", "workspace_size", "wait_selftest",
            "shared_mlp", "moe_mlp_forward", "mlp_workspace_size", "expert_forward_noalloc",
-           "moe_forward_shard", "moe_forward_shard_routed", "cast_output", "moe_backward"]
+           "moe_forward_shard", "moe_forward_shard_routed", "cast_output", "moe_backward",
+           "grouped_linear", "grouped_linear_backward", "quantize_rows", "quantized_linear"]
 
 
 @dataclass(frozen=True)
@@ -488,6 +492,166 @@ def token_centric_forward(D: LayerDims, x, W, V, idx, gate, *, U=None, y=None, c
     _lib.check(fn, getattr(_lib.load(), fn)(
         C.byref(dd), _ptr(x), *wts, _ptr(idx), _ptr(gate), _ptr(y), _ptr(counts),
         None, 0, _stream(stream)))
+    return y
+
+
+_OUT = {torch.float32: OMNI_F32, torch.bfloat16: OMNI_BF16}
+
+
+def _out_code(name, dtype):
+    if dtype not in _OUT:
+        raise ValueError(f"{name}: dtype {dtype}, the call writes float32 or bfloat16")
+    return _OUT[dtype]
+
+
+def _linear_setup(x, W, group_off, ids, n_groups, rows, dtype, others, names=("x", "W")):
+    """The checks the grouped products share; (dims, device) of a call of
+    x [T, in] with W [E, out, in] of the given dtype."""
+    i32 = torch.int32
+    for name, t, nd in ((names[0], x, 2), (names[1], W, 3)):
+        if t.dtype != dtype:
+            raise ValueError(f"{name}: dtype {t.dtype}, the call reads {dtype}")
+        if t.dim() != nd:
+            raise ValueError(f"{name}: {t.dim()} dimensions, the call reads {nd}")
+    if x.shape[1] != W.shape[2]:
+        raise ValueError(f"{names[0]}: rows of {x.shape[1]} elements, {names[1]} takes "
+                         f"{W.shape[2]}")
+    dev = x.device
+    G = 1 if group_off is None else group_off.numel() - 1
+    if group_off is not None:
+        _expect("group_off", group_off, 2, i32)
+    _expect("ids", ids, G, i32, optional=True)
+    _expect("n_groups", n_groups, 1, i32, optional=True)
+    _expect("rows", rows, 0, i32, optional=True)
+    for name, t in ((names[1], W), ("group_off", group_off), ("ids", ids),
+                    ("n_groups", n_groups), ("rows", rows), *others):
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name}: on {t.device}, {names[0]} is on {dev}")
+    M = x.shape[0] if rows is None else rows.numel()
+    return _lib.LinearDims(M, x.shape[0], x.shape[1], W.shape[1], W.shape[0], G), dev
+
+
+def _on(dev, stream, fn, args):
+    """Run a library call with dev current, on stream (default: dev's current one)."""
+    with torch.cuda.device(dev):
+        s = torch.cuda.current_stream(dev) if stream is None else stream
+        _lib.check(fn, getattr(_lib.load(), fn)(*args, C.c_void_p(s.cuda_stream)))
+
+
+def _linear_out(name, t, M, width, dtype, dev):
+    """The output [M, width]: t if given (its dtype is the call's), else a new
+    tensor of dtype."""
+    if t is None:
+        _out_code("out_dtype", dtype)
+        return torch.empty((M, width), dtype=dtype, device=dev)
+    _out_code(name, t.dtype)
+    _expect(name, t, M * width, t.dtype)
+    return t
+
+
+def grouped_linear(x, W, group_off, *, ids=None, n_groups=None, rows=None, silu=False, y=None,
+                   out_dtype=torch.bfloat16, counts=None, stream=None):
+    """Products of wide experts, rows grouped by expert: y[r] = x[rows[r]] . W[e]^T for the
+    rows r in [group_off[g], group_off[g + 1]) of each group g, e = ids[g] (SiLU of it with
+    silu).  x [T, in], W [E, out, in] bf16; group_off int32 [G + 1], ids int32 [G] (default:
+    matrix g), n_groups int32 [1] (default: all G), rows int32 [M] (default: row r of x).
+    A schedule with B = 1 has them: group_off, uniq, counts[1:2] and task_token.  Returns
+    y [M, out] in out_dtype (bf16 or fp32; of the given y, its own); rows in no group are
+    left as they were."""
+    D, dev = _linear_setup(x, W, group_off, ids, n_groups, rows, torch.bfloat16,
+                           (("y", y), ("counts", counts)))
+    _expect("counts", counts, 4, torch.int32, optional=True)
+    y = _linear_out("y", y, D.M, D.out, out_dtype, dev)
+    D.out_dtype, D.flags = _out_code("y", y.dtype), OMNI_LINEAR_SILU if silu else 0
+    _on(dev, stream, "omni_grouped_linear",
+        (C.byref(D), _ptr(x), _ptr(W), _ptr(group_off), _ptr(ids), _ptr(n_groups), _ptr(rows),
+         _ptr(y), _ptr(counts)))
+    return y
+
+
+def grouped_linear_backward(x, W, dy, group_off, *, ids=None, n_groups=None, rows=None,
+                            dx=None, dW=None, need_dx=True, need_dW=True,
+                            out_dtype=torch.bfloat16, accumulate=True, counts=None,
+                            stream=None):
+    """Gradients of the loss sum(dy * y) of grouped_linear (without silu): dx [M, in], one row
+    per product row (out_dtype, overwritten; with rows, add up the rows of a token), and
+    dW [E, out, in] fp32.  A given dW is added to (accumulate) or overwritten (the matrices of
+    no group are left as they were either way); without one, a new dW holds zeros there.
+    Returns a dict of those asked for."""
+    D, dev = _linear_setup(x, W, group_off, ids, n_groups, rows, torch.bfloat16,
+                           (("dy", dy), ("dx", dx), ("dW", dW), ("counts", counts)))
+    _expect("dy", dy, D.M * D.out, torch.bfloat16)
+    _expect("counts", counts, 4, torch.int32, optional=True)
+    if not (need_dx or need_dW):
+        raise ValueError("need_dx and need_dW: no gradient asked for")
+    g = {}
+    if need_dx:
+        g["dx"] = _linear_out("dx", dx, D.M, D.in_, out_dtype, dev)
+        D.out_dtype = _out_code("dx", g["dx"].dtype)
+    if need_dW:
+        if dW is None:
+            # with ids or n_groups some matrices may be in no group
+            make = torch.empty if ids is None and n_groups is None and D.G == D.E \
+                else torch.zeros
+            g["dW"], accumulate = make(W.shape, dtype=torch.float32, device=dev), False
+        else:
+            _expect("dW", dW, W.numel(), torch.float32)
+            g["dW"] = dW
+    _on(dev, stream, "omni_grouped_linear_backward",
+        (C.byref(D), _ptr(x), _ptr(W), _ptr(dy), _ptr(group_off), _ptr(ids), _ptr(n_groups),
+         _ptr(rows), _ptr(g.get("dx")), _ptr(g.get("dW")), 1 if accumulate else 0,
+         _ptr(counts)))
+    return g
+
+
+def quantize_rows(x, *, q=None, scale=None, stream=None):
+    """Rows to 8-bit integers with one scale each: (q int8 like x, scale f32 [x.shape[:-1]]),
+    scale = max|row| / 127, q = the integer nearest to x / scale (exactly; ties to even).
+    x bf16 or f32 [..., width]: tokens [T, in] or weights [E, out, in].  A row with an
+    infinity or a NaN gets scale NaN."""
+    code = _out_code("x", x.dtype)
+    if x.dim() < 1:
+        raise ValueError("x: 0 dimensions, the call reads rows")
+    width = x.shape[-1]
+    n = x.numel() // max(width, 1)
+    _expect("q", q, x.numel(), torch.int8, optional=True)
+    _expect("scale", scale, n, torch.float32, optional=True)
+    dev = x.device
+    for name, t in (("q", q), ("scale", scale)):
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name}: on {t.device}, x is on {dev}")
+    if q is None:
+        q = torch.empty(x.shape, dtype=torch.int8, device=dev)
+    if scale is None:
+        scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+    _on(dev, stream, "omni_quantize_rows", (n, width, code, _ptr(x), _ptr(q), _ptr(scale)))
+    return q, scale
+
+
+def quantized_linear(xq, xs, Wq, Ws, group_off=None, *, ids=None, n_groups=None, rows=None,
+                     silu=False, y=None, out_dtype=torch.bfloat16, counts=None, stream=None):
+    """Products of 8-bit integers with a scale per token and per output channel:
+    y[r, f] = xs[t] * Ws[f] * sum_c xq[t, c] * Wq[f, c] (SiLU of it with silu), t = rows[r]
+    (default r).  xq int8 [T, in], xs f32 [T] and Wq int8, Ws f32 as quantize_rows makes
+    them: one matrix Wq [out, in], or by expert Wq [E, out, in] with the group arrays of
+    grouped_linear.  Returns y [M, out] in out_dtype (bf16 or fp32; of the given y, its own)."""
+    if group_off is None:
+        if Wq.dim() != 2:
+            raise ValueError(f"Wq: {Wq.dim()} dimensions, the call without group_off reads 2")
+        if ids is not None or n_groups is not None:
+            raise ValueError("group_off is required with ids or n_groups")
+        Wq = Wq.unsqueeze(0)
+    D, dev = _linear_setup(xq, Wq, group_off, ids, n_groups, rows, torch.int8,
+                           (("xs", xs), ("Ws", Ws), ("y", y), ("counts", counts)),
+                           names=("xq", "Wq"))
+    _expect("xs", xs, D.T, torch.float32)
+    _expect("Ws", Ws, D.E * D.out, torch.float32)
+    _expect("counts", counts, 4, torch.int32, optional=True)
+    y = _linear_out("y", y, D.M, D.out, out_dtype, dev)
+    D.out_dtype, D.flags = _out_code("y", y.dtype), OMNI_LINEAR_SILU if silu else 0
+    _on(dev, stream, "omni_quantized_linear",
+        (C.byref(D), _ptr(xq), _ptr(xs), _ptr(Wq), _ptr(Ws), _ptr(group_off), _ptr(ids),
+         _ptr(n_groups), _ptr(rows), _ptr(y), _ptr(counts)))
     return y
 
 

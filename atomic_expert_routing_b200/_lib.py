@@ -22,6 +22,9 @@ OMNI_FLAG_ROUTER_SIMT = 1
 OMNI_FLAG_STAGED_SMALL = 2
 OMNI_FLAG_DENSE_TENSOR_CORES = 4
 
+OMNI_LINEAR_SILU = 1
+OMNI_MAX_GROUPS = 1024
+
 OMNI_WS_ROUTE = 0
 OMNI_WS_SCHEDULE = 1
 OMNI_WS_EXPERT = 2
@@ -56,6 +59,10 @@ SIGNATURES = {
     "omni_wait_selftest": ([_P, _P], C.c_int),
     "omni_shared_mlp": ([_P, _I64, _P, _P, _P, _P, C.c_int, _P, _P, C.c_size_t, _P], C.c_int),
     "omni_moe_mlp_forward": ([_P, _I64] + [_P] * 14 + [C.c_size_t, _P], C.c_int),
+    "omni_grouped_linear": ([_P] * 10, C.c_int),
+    "omni_grouped_linear_backward": ([_P] * 10 + [C.c_int, _P, _P], C.c_int),
+    "omni_quantize_rows": ([_I64, _I64, C.c_int] + [_P] * 4, C.c_int),
+    "omni_quantized_linear": ([_P] * 12, C.c_int),
     "omni_mlp_workspace_size": ([_P, _I64, C.c_int, C.POINTER(C.c_size_t)], C.c_int),
 }
 
@@ -63,6 +70,12 @@ SIGNATURES = {
 class Dims(C.Structure):
     _fields_ = [("L", C.c_int64), ("d", C.c_int64), ("Nr", C.c_int64), ("Nc", C.c_int64),
                 ("k", C.c_int64), ("K", C.c_int64), ("B", C.c_int64), ("dtype", C.c_int32),
+                ("flags", C.c_int32)]
+
+
+class LinearDims(C.Structure):
+    _fields_ = [("M", C.c_int64), ("T", C.c_int64), ("in_", C.c_int64), ("out", C.c_int64),
+                ("E", C.c_int64), ("G", C.c_int64), ("out_dtype", C.c_int32),
                 ("flags", C.c_int32)]
 
 

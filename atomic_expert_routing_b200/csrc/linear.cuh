@@ -1,0 +1,170 @@
+// Grouped products (the wide experts and the 8-bit products): what a launch
+// gets, and the group table every CTA builds from the caller's device arrays.
+#pragma once
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace omni {
+
+// One group as the kernels see it: its first tile, rows and matrix.
+struct __align__(16) GroupTab {
+  int32_t begin;  // tiles of all earlier groups
+  int32_t row0;   // first product row
+  int32_t rows;
+  int32_t id;     // matrix
+};
+
+// The group arrays of a call (device pointers, see include/omnimoe.h).
+struct Groups {
+  int64_t M;
+  int32_t E, G;
+  const int32_t* off;       // nullptr: one group of all M rows
+  const int32_t* ids;       // nullptr: matrix g
+  const int32_t* n_groups;  // nullptr: G
+};
+
+// Shared memory of build_groups beside the table: per-warp partial results
+// and the totals.
+struct GroupScratch {
+  int32_t off_max[32], id_max[32], tiles[32], used[32];
+  int32_t total_tiles, total_groups;
+};
+
+// Builds the table of the groups that have tiles, in order, with every
+// thread of the CTA (blockDim.x a multiple of 32, at most 1024); ends with a
+// CTA barrier.  tiles_of(rows): tiles of a group of that many rows, 0 to
+// leave it out.  A group counts only if its first offset is the largest
+// entry so far, its end is neither before that nor past M, and its id lies
+// in [0, E) above every earlier id: no two listed groups then share a row or
+// a matrix, whatever the arrays hold (G <= E, so without ids group g's is g).  status: where the bad-index bit goes
+// (one CTA passes it, the others nullptr).
+template <class TilesOf>
+__device__ __forceinline__ void build_groups(const Groups& P, const TilesOf& tiles_of,
+                                             GroupTab* tab, GroupScratch* sh, int32_t* status) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nwarps = blockDim.x >> 5;
+  if (P.off == nullptr) {
+    if (tid == 0) {
+      const int32_t rows = static_cast<int32_t>(P.M);
+      tab[0] = GroupTab{0, 0, rows, 0};
+      sh->total_tiles = tiles_of(rows);
+      sh->total_groups = sh->total_tiles > 0 ? 1 : 0;
+    }
+    __syncthreads();
+    return;
+  }
+  int n = P.G;
+  bool bad = false;
+  if (P.n_groups != nullptr) {
+    const int v = *P.n_groups;
+    bad = v < 0 || v > n;
+    n = v < 0 ? 0 : (v > n ? n : v);
+  }
+  int32_t carry_off = 0, carry_id = -1, carry_tiles = 0, carry_used = 0;
+  for (int g0 = 0; g0 < n; g0 += blockDim.x) {
+    const int g = g0 + tid;
+    const bool in = g < n;
+    const int32_t a = in ? P.off[g] : 0;
+    const int32_t b = in ? P.off[g + 1] : 0;
+    const int32_t id = in ? (P.ids != nullptr ? P.ids[g] : g) : -1;
+    // running maxima of the offsets (inclusive) and ids (exclusive)
+    int32_t mo = a, mi = id;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int32_t po = __shfl_up_sync(0xffffffffu, mo, o);
+      const int32_t pi = __shfl_up_sync(0xffffffffu, mi, o);
+      if (lane >= o) {
+        mo = po > mo ? po : mo;
+        mi = pi > mi ? pi : mi;
+      }
+    }
+    if (lane == 31) {
+      sh->off_max[warp] = mo;
+      sh->id_max[warp] = mi;
+    }
+    int32_t mi_before = __shfl_up_sync(0xffffffffu, mi, 1);
+    if (lane == 0) mi_before = -1;
+    __syncthreads();
+    int32_t all_off = carry_off, all_id = carry_id;
+    int32_t before_off = carry_off, before_id = carry_id;
+    for (int w = 0; w < nwarps; ++w) {
+      if (w == warp) {
+        before_off = all_off;
+        before_id = all_id;
+      }
+      all_off = sh->off_max[w] > all_off ? sh->off_max[w] : all_off;
+      all_id = sh->id_max[w] > all_id ? sh->id_max[w] : all_id;
+    }
+    carry_off = all_off;
+    carry_id = all_id;
+    mo = before_off > mo ? before_off : mo;
+    mi_before = before_id > mi_before ? before_id : mi_before;
+    const bool ok = in && a >= 0 && a == mo && b >= a && b <= P.M && id >= 0 && id < P.E &&
+                    id > mi_before;
+    bad |= in && !ok;
+    // places in the table; a bad group whose matrix is known is one without rows
+    const int32_t rows = ok ? b - a : 0;
+    const int32_t mine = ok || (in && P.ids == nullptr) ? tiles_of(rows) : 0;
+    int32_t st = mine, su = mine > 0 ? 1 : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int32_t pt = __shfl_up_sync(0xffffffffu, st, o);
+      const int32_t pu = __shfl_up_sync(0xffffffffu, su, o);
+      if (lane >= o) {
+        st += pt;
+        su += pu;
+      }
+    }
+    if (lane == 31) {
+      sh->tiles[warp] = st;
+      sh->used[warp] = su;
+    }
+    __syncthreads();
+    int32_t before_t = 0, before_u = 0, all_t = 0, all_u = 0;
+    for (int w = 0; w < nwarps; ++w) {
+      if (w == warp) {
+        before_t = all_t;
+        before_u = all_u;
+      }
+      all_t += sh->tiles[w];
+      all_u += sh->used[w];
+    }
+    if (mine > 0)
+      tab[carry_used + before_u + su - 1] =
+          GroupTab{carry_tiles + before_t + st - mine, a, rows, id};
+    carry_tiles += all_t;
+    carry_used += all_u;
+    // the next round writes the maxima before its first barrier and the sums
+    // after it: every thread is past its reads of both by then
+  }
+  if (tid == 0) {
+    sh->total_tiles = carry_tiles;
+    sh->total_groups = carry_used;
+  }
+  if (bad) raise_status(status, OMNI_DEV_BAD_INDEX);
+  __syncthreads();
+}
+
+// What the products of one launch read and write.
+struct LinearArgs {
+  Groups g;
+  int64_t T;
+  int32_t in, out;
+  int32_t out_f32, silu, accumulate;
+  const int32_t* rows;  // nullable
+  const void* x;        // [T x in]
+  const void* W;        // [E x out x in]
+  const void* dy;       // [M x out]
+  const float* xs;      // [T] (8-bit products)
+  const float* Ws;      // [E x out]
+  void* o;              // y [M x out], dx [M x in] or dW [E x out x in]
+  int32_t* status;
+};
+
+enum class Product { kForward, kGradX, kGradW, kInt8 };
+
+cudaError_t launch_linear(Product p, const LinearArgs& a, cudaStream_t s);
+cudaError_t launch_quantize_rows(int64_t n, int64_t width, bool f32, const void* src, int8_t* q,
+                                 float* scale, cudaStream_t s);
+
+}  // namespace omni

@@ -86,9 +86,13 @@ extern "C" {
                                           B <= 128 experts) are formed on the tensor cores;
                                           counts[3] receives how many groups were */
 
+/* omni_linear_dims.flags bits */
+#define OMNI_LINEAR_SILU 1      /* y = SiLU(product) (forward calls only) */
+
 /* Limits of this build (host checks return OMNI_ERR_UNSUPPORTED beyond them). */
 #define OMNI_MAX_AXIS 4096      /* Nr, Nc */
 #define OMNI_MAX_TOPK 256       /* k, K */
+#define OMNI_MAX_GROUPS 1024    /* G of omni_linear_dims */
 
 /* Host checks of omni_dims, made by every call that takes dims.
  * A field outside its range returns OMNI_ERR_INVALID_ARG:
@@ -407,6 +411,102 @@ int omni_moe_backward(const omni_dims* dims, const void* x, const void* Wr, cons
                       const void* dy, float* dx, float* dW, float* dV, float* dWr, float* dWc,
                       float* dbias_r, float* dbias_c, int accumulate, int32_t* counts, void* ws,
                       size_t ws_bytes, void* stream);
+
+/* ---- wide experts and 8-bit products --------------------------------------
+ *
+ * The pages' experts are vector pairs; these calls run experts (or one
+ * matrix) of any width behind the same router and scheduler.  Expert e is a
+ * matrix W[e] [out x in]; the M product rows come in groups, one expert each,
+ * of any sizes, one after another: group g holds the rows
+ * [group_off[g], group_off[g + 1]) and takes matrix ids[g] (ids == NULL:
+ * matrix g).  omni_schedule with B = 1 leaves exactly these arrays: group_off,
+ * ids = uniq, rows = task_token, n_groups = counts + 1.
+ */
+typedef struct omni_linear_dims {
+  int64_t M;         /* product rows (>= 0) */
+  int64_t T;         /* rows of x (== M when rows == NULL) */
+  int64_t in;        /* width of x's rows */
+  int64_t out;       /* width of y's rows */
+  int64_t E;         /* weight matrices */
+  int64_t G;         /* groups: group_off has G + 1 entries, ids has G; G <= E */
+  int32_t out_dtype; /* OMNI_F32 or OMNI_BF16: the type of y (of dx) */
+  int32_t flags;     /* OMNI_LINEAR_* */
+} omni_linear_dims;
+
+/* Host checks of omni_linear_dims, made by every call that takes them.
+ * OMNI_ERR_INVALID_ARG: M < 0; T, in, out, E or G < 1 (T < 0 when M == 0);
+ *   G > E; an unknown out_dtype or flag; T != M without rows.
+ * OMNI_ERR_UNSUPPORTED: G > OMNI_MAX_GROUPS; in or out > 65536; in or out not
+ *   a multiple of 8 (in of the 8-bit product: of 16); M, T or E >= 2^30.
+ * When both apply, OMNI_ERR_INVALID_ARG is returned.
+ *
+ * Device arrays the calls below read (4-byte aligned; all other arrays 16):
+ *   group_off int32 [G + 1]  ascending offsets into [0, M]
+ *   ids       int32 [G], nullable  strictly ascending matrix ids
+ *   n_groups  int32 [1], nullable  how many of the G groups there are (the
+ *             entries of group_off and ids behind them are not used)
+ *   rows      int32 [M], nullable  the row of x each product row takes, so
+ *             that tokens need not be copied into expert order first
+ *   counts    int32 [4], nullable  counts[2] receives the status bits
+ * Rows of y (dx) in no group are left as they were.  What is read on the
+ * device is checked there: an offset below an earlier one or outside [0, M],
+ * an id outside [0, E) or not above every earlier id, or a group count
+ * outside [0, G] (clamped) sets OMNI_DEV_BAD_INDEX, and the group is left
+ * out (without ids its dW is that of a group without rows); so does an entry of rows outside [0, T), which is taken as row 0.
+ * The calls need no workspace. */
+
+/*
+ * y[r] = x[rows[r]] . W[e]^T for every row r of the group of expert e, SiLU
+ * of it with OMNI_LINEAR_SILU.  x [T x in], W [E x out x in] bf16, y [M x out]
+ * in out_dtype; fp32 sums, one rounding.
+ */
+int omni_grouped_linear(const omni_linear_dims* dims, const void* x, const void* W,
+                        const int32_t* group_off, const int32_t* ids, const int32_t* n_groups,
+                        const int32_t* rows, void* y, int32_t* counts, void* stream);
+
+/*
+ * Backward of omni_grouped_linear without SiLU: for the loss sum(dy * y),
+ *   dx[r] = dy[r] . W[e]   [M x in] in out_dtype, one row per PRODUCT row
+ *           (with rows: the caller sums the rows of one token), overwritten;
+ *   dW[e] = sum over the rows r of e's group of dy[r]^T x[rows[r]],
+ *           [E x out x in] fp32: added to when accumulate != 0, else
+ *           overwritten (with zeros for a group without rows).  Matrices of
+ *           no group are left as they were.
+ * dx or dW may be NULL (not both): that gradient is not formed, and what only
+ * it reads (W for dx; x and rows for dW) may be NULL too.  dy [M x out] bf16.
+ * OMNI_LINEAR_SILU returns OMNI_ERR_UNSUPPORTED.
+ */
+int omni_grouped_linear_backward(const omni_linear_dims* dims, const void* x, const void* W,
+                                 const void* dy, const int32_t* group_off, const int32_t* ids,
+                                 const int32_t* n_groups, const int32_t* rows, void* dx,
+                                 float* dW, int accumulate, int32_t* counts, void* stream);
+
+/*
+ * Rows to 8-bit integers with one scale each: scale[r] = max_c |src[r, c]| / 127
+ * rounded to fp32, q[r, c] the integer in [-127, 127] nearest to
+ * src[r, c] / scale[r] (the exact quotient; ties to even).  A row of zeros
+ * gets scale 0 and zeros; a row with an infinity or a NaN gets scale NaN and
+ * zeros, so that its products are NaN.
+ *   src [n x width] of dtype OMNI_BF16 or OMNI_F32, q int8 [n x width],
+ *   scale float [n].  width a multiple of 16 and at most 65536, n < 2^30.
+ * For the tokens of omni_quantized_linear when it is called, and for its
+ * weights (n = E * out rows) once.
+ */
+int omni_quantize_rows(int64_t n, int64_t width, int dtype, const void* src, int8_t* q,
+                       float* scale, void* stream);
+
+/*
+ * The product of 8-bit integers with a scale per token and per channel:
+ *   y[r, f] = xs[t] * Ws[e, f] * sum_c xq[t, c] * Wq[e, f, c],  t = rows[r]
+ * (SiLU of it with OMNI_LINEAR_SILU).  xq int8 [T x in], xs float [T],
+ * Wq int8 [E x out x in], Ws float [E x out], y [M x out] in out_dtype.
+ * The integer sums are exact (32 bits: in <= 65536).  group_off == NULL: one
+ * matrix for every row (E == G == 1, ids and n_groups NULL).
+ */
+int omni_quantized_linear(const omni_linear_dims* dims, const int8_t* xq, const float* xs,
+                          const int8_t* Wq, const float* Ws, const int32_t* group_off,
+                          const int32_t* ids, const int32_t* n_groups, const int32_t* rows,
+                          void* y, int32_t* counts, void* stream);
 
 /* Static description of a status code (never NULL). */
 const char* omni_status_string(int status);
