@@ -1,169 +1,8 @@
-// The products of wide experts and of 8-bit integers: entry points
-// (include/omnimoe.h) and kernels.
-//
-// Every product is D[j, i] = sum_k B[j, k] A[i, k] over the tiles of a group:
-//   forward, 8-bit: j a product row, i an output channel, k an input channel;
-//   dx:             j a product row, i an input channel, k an output channel;
-//   dW:             j an output channel, i an input channel, k a product row.
-// A CTA takes 64 x 64 tiles of all groups in turn, 16 of k at a time through
-// shared memory, 4 x 4 sums per thread, in pieces of 512 products (a long sum's
-// rounding then grows with the pieces, not with the products).
+// The products of wide experts and of 8-bit integers: the entry points of
+// include/omnimoe.h and their host checks (kernels: linear_tc.cu, quantize.cu).
 #include "linear.cuh"
 
 namespace omni {
-namespace {
-
-constexpr int kTile = 64, kStep = 16, kThreads = 256;
-constexpr int kPiece = 512;  // products summed before they join the running sum
-
-template <Product P>
-__global__ void __launch_bounds__(kThreads) k_linear(const LinearArgs a) {
-  extern __shared__ GroupTab tab[];
-  __shared__ GroupScratch sh;
-  __shared__ float sa[kStep][kTile + 1], sb[kStep][kTile + 1];
-  __shared__ int32_t src_row[kTile];
-  pdl_wait();
-  constexpr bool kGradW = P == Product::kGradW;
-  constexpr bool kGradX = P == Product::kGradX;
-  const int I = kGradX || kGradW ? a.in : a.out;
-  const int mt = (I + kTile - 1) / kTile;
-  int32_t* status = blockIdx.x == 0 ? a.status : nullptr;
-  build_groups(
-      a.g,
-      [&](int rows) {
-        if (kGradW)
-          return rows > 0 || !a.accumulate ? mt * ((a.out + kTile - 1) / kTile) : 0;
-        return mt * ((rows + kTile - 1) / kTile);
-      },
-      tab, &sh, status);
-  const int tiles = sh.total_tiles;
-  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  int c = 0;
-  for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
-    while (c + 1 < sh.total_groups && tab[c + 1].begin <= t) ++c;
-    const GroupTab gr = tab[c];
-    const int local = t - gr.begin;
-    const int i0 = (local % mt) * kTile, j0 = (local / mt) * kTile;
-    const int J = kGradW ? a.out : gr.rows;
-    const int K = kGradW ? gr.rows : kGradX ? a.out : a.in;
-    const int64_t wbase = static_cast<int64_t>(gr.id) * a.out * a.in;
-    auto token = [&](int r) -> int64_t {  // product row (of this group) -> row of x
-      const int64_t m = gr.row0 + r;
-      if (a.rows == nullptr) return m;
-      const int32_t v = a.rows[m];
-      if (v < 0 || v >= a.T) {
-        raise_status(a.status, OMNI_DEV_BAD_INDEX);
-        return 0;
-      }
-      return v;
-    };
-    if constexpr (!kGradW && !kGradX) {
-      if (tid < kTile) src_row[tid] = j0 + tid < J ? static_cast<int32_t>(token(j0 + tid)) : 0;
-      __syncthreads();
-    }
-    float acc[4][4] = {}, sum[4][4] = {};
-    int isum[4][4] = {};
-    for (int k0 = 0; k0 < K; k0 += kStep) {
-      for (int q = tid; q < kStep * kTile; q += kThreads) {
-        // k fastest where it is contiguous in memory
-        const int kk = kGradW ? q / kTile : q % kStep, u = kGradW ? q % kTile : q / kStep;
-        const int k = k0 + kk, i = i0 + u, j = j0 + u;
-        float va = 0.0f, vb = 0.0f;
-        if (k < K) {
-          if constexpr (P == Product::kForward) {
-            if (i < I) va = to_float(static_cast<const __nv_bfloat16*>(a.W)[wbase + int64_t(i) * a.in + k]);
-            if (j < J) vb = to_float(static_cast<const __nv_bfloat16*>(a.x)[int64_t(src_row[u]) * a.in + k]);
-          } else if constexpr (P == Product::kInt8) {
-            if (i < I) va = static_cast<const int8_t*>(a.W)[wbase + int64_t(i) * a.in + k];
-            if (j < J) vb = static_cast<const int8_t*>(a.x)[int64_t(src_row[u]) * a.in + k];
-          } else if constexpr (kGradX) {
-            if (i < I) va = to_float(static_cast<const __nv_bfloat16*>(a.W)[wbase + int64_t(k) * a.in + i]);
-            if (j < J) vb = to_float(static_cast<const __nv_bfloat16*>(a.dy)[int64_t(gr.row0 + j) * a.out + k]);
-          } else {
-            if (i < I) va = to_float(static_cast<const __nv_bfloat16*>(a.x)[token(k) * a.in + i]);
-            if (j < J) vb = to_float(static_cast<const __nv_bfloat16*>(a.dy)[int64_t(gr.row0 + k) * a.out + j]);
-          }
-        }
-        sa[kk][u] = va;
-        sb[kk][u] = vb;
-      }
-      __syncthreads();
-#pragma unroll
-      for (int kk = 0; kk < kStep; ++kk) {
-        float fa[4], fb[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          fa[u] = sa[kk][tx + 16 * u];
-          fb[u] = sb[kk][ty + 16 * u];
-        }
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-#pragma unroll
-          for (int v = 0; v < 4; ++v) acc[u][v] = fmaf(fb[u], fa[v], acc[u][v]);
-      }
-      __syncthreads();
-      if constexpr (P == Product::kInt8) {
-        // a step's sum is exact in fp32 (16 * 127^2 < 2^24); the whole sum needs integers
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-#pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            isum[u][v] += static_cast<int>(acc[u][v]);
-            acc[u][v] = 0.0f;
-          }
-      } else if ((k0 + kStep) % kPiece == 0 || k0 + kStep >= K) {
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-#pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            sum[u][v] += acc[u][v];
-            acc[u][v] = 0.0f;
-          }
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int j = j0 + ty + 16 * u;
-      if (j >= J) continue;
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const int i = i0 + tx + 16 * v;
-        if (i >= I) continue;
-        if constexpr (kGradW) {
-          float* o = static_cast<float*>(a.o) + wbase + int64_t(j) * a.in + i;
-          *o = a.accumulate ? *o + sum[u][v] : sum[u][v];
-        } else {
-          float z = sum[u][v];
-          if constexpr (P == Product::kInt8)
-            z = static_cast<float>(isum[u][v]) * a.xs[src_row[ty + 16 * u]] *
-                a.Ws[int64_t(gr.id) * a.out + i];
-          if (a.silu) z = silu(z);
-          const int64_t at = int64_t(gr.row0 + j) * I + i;
-          if (a.out_f32) static_cast<float*>(a.o)[at] = z;
-          else static_cast<__nv_bfloat16*>(a.o)[at] = __float2bfloat16_rn(z);
-        }
-      }
-    }
-    if constexpr (!kGradW && !kGradX) __syncthreads();  // src_row is the next tile's
-  }
-}
-
-}  // namespace
-
-cudaError_t launch_linear(Product p, const LinearArgs& a, cudaStream_t s) {
-  auto go = [&](auto kernel) -> cudaError_t {
-    const size_t smem = sizeof(GroupTab) * static_cast<size_t>(a.g.G);
-    OMNI_TRY(launch_k(kernel, 148 * 4, kThreads, smem, s, a));
-    return cudaGetLastError();
-  };
-  switch (p) {
-    case Product::kForward: return go(k_linear<Product::kForward>);
-    case Product::kGradX: return go(k_linear<Product::kGradX>);
-    case Product::kGradW: return go(k_linear<Product::kGradW>);
-    default: return go(k_linear<Product::kInt8>);
-  }
-}
-
 namespace {
 
 bool aligned(const void* p, uintptr_t a) {

@@ -1,0 +1,699 @@
+// The products of wide experts and of 8-bit integers on the 5th-generation
+// tensor cores.
+//
+// Every product is D[j, i] = sum_k B[j, k] A[i, k] over the tiles of a group:
+//   forward, 8-bit: j a product row, i an output channel, k an input channel;
+//   dx:             j a product row, i an input channel, k an output channel;
+//   dW:             j an output channel, i an input channel, k a product row.
+// i, the axis that is contiguous in the result, takes the MMA's M (128 per
+// CTA: a TMEM lane each, so a warp's stores are contiguous); j takes its N,
+// which is as wide as the group's rows need in steps of 16 per CTA.  A group
+// that ends inside a tile then costs no idle products, and a decode batch's
+// few rows per expert are an MMA of N = 16 or 32 over the streamed weights.
+// Rows past a group's end that a load brings along only reach columns that
+// are not stored; dW, whose sum runs over the rows, loads its last rows one
+// by one and reads zeros behind them.
+//
+// Operands come by TMA in 128-byte-swizzled tiles of 128 bytes of k (K-major)
+// or of 64 x 64 (the transposed operands of dx and dW, MN-major), rows by
+// token with gather4.  CTAS = 2 pairs two CTAs on one 256-wide tile: each
+// holds its half of A and of B, and the pair's first CTA issues the MMAs.
+// Warps 0-7 drain the accumulators, warp 8 loads, warp 9 issues; two TMEM
+// accumulators alternate, so a tile is stored while the next is summed.
+//
+// PIECES: the tensor core's fp32 sums cut every addition towards zero, an
+// error of about 1.1e-9 of the result per term of k.  bf16 results do not
+// show it; fp32 results are summed in pieces of 512 terms, which the draining
+// warps add up in registers, rounded to nearest.
+#include "linear.cuh"
+#include "tc_common.cuh"
+
+namespace omni {
+namespace {
+
+using namespace tc;
+
+constexpr int kBM = 128;            // i per CTA
+constexpr int kABytes = kBM * 128;  // a stage's A tile: 128 bytes of k per row
+constexpr int kMaxStages = 12;
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 32 * (kEpiWarps + 2);
+constexpr int kPieceBlocks = 8;     // k-blocks of 64 in a piece
+constexpr size_t kSmemLimit = 227 * 1024;
+
+// ---- instructions --------------------------------------------------------------
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+}
+// the address of the first CTA's copy of a shared-memory location of this one
+__device__ __forceinline__ uint32_t leader_addr(uint32_t a) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(a));
+  return r;
+}
+
+// bar: an mbarrier of this CTA, or with CTAS == 2 of either
+template <int CTAS>
+__device__ __forceinline__ void load_2d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0,
+                                        int c1) {
+  if constexpr (CTAS == 1)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst), "l"(m), "r"(bar), "r"(c0), "r"(c1)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        ".cta_group::2 [%0], [%1, {%3, %4}], [%2];" ::"r"(dst), "l"(m), "r"(bar), "r"(c0),
+        "r"(c1)
+        : "memory");
+}
+template <int CTAS>
+__device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0,
+                                        int c1, int c2) {
+  if constexpr (CTAS == 1)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst), "l"(m), "r"(bar), "r"(c0), "r"(c1),
+        "r"(c2)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        ".cta_group::2 [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst), "l"(m), "r"(bar), "r"(c0),
+        "r"(c1), "r"(c2)
+        : "memory");
+}
+// four rows r of a map whose box is one row high
+template <int CTAS>
+__device__ __forceinline__ void load_rows4(uint32_t dst, const CUtensorMap* m, uint32_t bar,
+                                           int c0, const int* r) {
+  if constexpr (CTAS == 1)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4"
+        ".mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
+        "l"(m), "r"(bar), "r"(c0), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4"
+        ".mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(
+            dst),
+        "l"(m), "r"(bar), "r"(c0), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+        : "memory");
+}
+
+template <int CTAS, bool I8>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                    uint32_t accumulate) {
+  if constexpr (CTAS == 1 && !I8)
+    umma_bf16(d, a, b, idesc, accumulate);
+  else if constexpr (!I8)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
+  else if constexpr (CTAS == 1)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
+}
+// arrive on bar (of both CTAs of a pair) once the MMAs issued so far are done
+template <int CTAS>
+__device__ __forceinline__ void commit(uint32_t bar) {
+  if constexpr (CTAS == 1)
+    umma_commit(bar);
+  else
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+        " [%0], %1;" ::"r"(bar),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+}
+template <int CTAS>
+__device__ __forceinline__ void tmem_alloc(uint32_t slot, uint32_t cols) {
+  if constexpr (CTAS == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot),
+                 "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot),
+                 "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+}
+template <int CTAS>
+__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
+  if constexpr (CTAS == 1)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols)
+                 : "memory");
+  else
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols)
+                 : "memory");
+}
+
+// Shared-memory descriptor of an MN-major tile with 128-byte swizzle: 64 of
+// the operand's M or N (128 bytes) per k, 8-k groups 1024 bytes apart, chunks
+// of 64 along M or N one [64 k x 128 bytes] box, 8192 bytes, apart.
+__device__ __forceinline__ uint64_t mn_desc(uint32_t saddr) {
+  return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) |
+         (static_cast<uint64_t>(8192 >> 4) << 16) | (static_cast<uint64_t>(1024 >> 4) << 32) |
+         (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
+}
+
+// ---- the kernel ------------------------------------------------------------------
+
+struct Maps {
+  CUtensorMap a, b;  // boxes of an operand's tile (a: W, or x for dW)
+  CUtensorMap rows;  // x's rows one by one (gathered, or the last of dW)
+  CUtensorMap brow;  // dy's rows one by one (the last of dW)
+};
+
+template <Product P, int CTAS, int BN, bool PIECES>
+struct Cfg {
+  static constexpr bool kI8 = P == Product::kInt8;
+  static constexpr bool kGradW = P == Product::kGradW, kGradX = P == Product::kGradX;
+  static constexpr bool kMnA = kGradW || kGradX, kMnB = kGradW;
+  static constexpr int kBlockK = kI8 ? 128 : 64;  // k per stage
+  static constexpr int kMmaK = kI8 ? 32 : 16;
+  static constexpr int kNb = BN / CTAS;           // j per CTA
+  static constexpr int kBox = kNb < 32 ? kNb : 32;  // rows of one B load
+  static constexpr int kBBytes = kNb * 128;
+  static constexpr int kStage = kABytes + kBBytes;
+  static constexpr int kCols = 2 * BN;            // TMEM columns
+  static_assert(!kGradW || kNb % 64 == 0, "dW's B tile is made of 64-wide boxes");
+};
+
+// One tile: columns j0 .. j0 + n - 1 of a group, i from i0.
+struct Tile {
+  int i0, j0, n, row0, id, K;
+};
+
+template <class C, int CTAS, int BN>
+struct TileWalk {
+  const LinearArgs& a;
+  const GroupTab* tab;
+  int groups, mt, c = 0;
+  __device__ __forceinline__ Tile at(int t) {
+    while (c + 1 < groups && tab[c + 1].begin <= t) ++c;
+    const GroupTab g = tab[c];
+    const int local = t - g.begin;
+    Tile r;
+    r.i0 = (local % mt) * (kBM * CTAS);
+    r.j0 = (local / mt) * BN;
+    const int J = C::kGradW ? a.out : g.rows;
+    r.n = J - r.j0 < BN ? J - r.j0 : BN;
+    r.row0 = g.row0;
+    r.id = g.id;
+    r.K = C::kGradW ? g.rows : C::kGradX ? a.out : a.in;
+    return r;
+  }
+};
+
+template <Product P, int CTAS, int BN, bool PIECES>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_linear_tc(const __grid_constant__ Maps maps, const __grid_constant__ LinearArgs a,
+                int stages) {
+  using C = Cfg<P, CTAS, BN, PIECES>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t bars[2 * kMaxStages + 5];
+  __shared__ uint32_t tmem_slot, aborted;
+  __shared__ GroupScratch scratch;
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const uint32_t sA = smem_u32(smem), sB = sA + stages * kABytes;
+  GroupTab* tab = reinterpret_cast<GroupTab*>(smem + stages * C::kStage);
+  const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * kMaxStages;
+  const uint32_t tfull0 = empty0 + 8 * kMaxStages, tempty0 = tfull0 + 16, drain = tempty0 + 16;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = CTAS == 2 ? static_cast<int>(cluster_rank()) : 0;
+  const int first = blockIdx.x / CTAS, step = gridDim.x / CTAS;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(full0 + 8 * s, 1);
+      mbar_init(empty0 + 8 * s, 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(tfull0 + 8 * b, 1);
+      mbar_init(tempty0 + 8 * b, kEpiWarps * CTAS);
+    }
+    mbar_init(drain, 1);
+    aborted = 0u;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  if (warp == kEpiWarps + 1) tmem_alloc<CTAS>(smem_u32(&tmem_slot), C::kCols);
+  pdl_wait();
+  const int I = C::kMnA ? a.in : a.out;
+  const int mt = (I + kBM * CTAS - 1) / (kBM * CTAS);
+  build_groups(
+      a.g,
+      [&](int rows) {
+        if (C::kGradW) return rows > 0 || !a.accumulate ? mt * ((a.out + BN - 1) / BN) : 0;
+        return mt * ((rows + BN - 1) / BN);
+      },
+      tab, &scratch, blockIdx.x == 0 ? a.status : nullptr);
+  const int tiles = scratch.total_tiles;
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  if (CTAS == 2) cluster_sync();
+  else __syncthreads();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  const uint32_t tmem = tmem_slot;
+  TileWalk<C, CTAS, BN> walk{a, tab, scratch.total_groups, mt};
+  auto n_mma = [](const Tile& t) { return (t.n + 16 * CTAS - 1) / (16 * CTAS) * (16 * CTAS); };
+
+  bool timed_out = false;
+  uint32_t issued = 0;  // stages loaded
+  if (warp == kEpiWarps) {
+    // ---- loads: lane 0, or every lane where rows are loaded one by one
+    int s = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    // a row of x by its place in the group order, checked
+    auto token = [&](int r, bool valid) -> int {
+      if (!valid) return 0;
+      const int v = a.rows[r];
+      if (v >= 0 && v < a.T) return v;
+      raise_status(a.status, OMNI_DEV_BAD_INDEX);
+      return 0;
+    };
+    for (int t = first; t < tiles && ok; t += step) {
+      const Tile tl = walk.at(t);
+      const int nb = n_mma(tl) / CTAS;  // j of this CTA: j0 + rank * nb ..
+      const int i0 = tl.i0 + rank * kBM, j0 = tl.j0 + rank * nb;
+      const int nk = (tl.K + C::kBlockK - 1) / C::kBlockK;
+      int idx[4] = {0, 0, 0, 0};
+      if (!C::kMnA && a.rows != nullptr) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          idx[q] = token(tl.row0 + j0 + 4 * lane + q, 4 * lane < nb && j0 + 4 * lane + q < tl.j0 + tl.n);
+      }
+      for (int kb = 0; kb < nk; ++kb) {
+        const uint32_t bar = CTAS == 2 ? leader_addr(full0 + 8 * s) : full0 + 8 * s;
+        const uint32_t da = sA + s * kABytes, db = sB + s * C::kBBytes;
+        const int k0 = kb * C::kBlockK;
+        const int left = tl.K - k0;
+        const bool one_by_one = C::kGradW && left < C::kBlockK;
+        if constexpr (C::kGradW) {
+          if (a.rows != nullptr) {  // the block's rows, read before its stage is free
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int r = 4 * (lane & 15) + q;
+              idx[q] = token(tl.row0 + k0 + r, r < left);
+            }
+          }
+        }
+        ok = __all_sync(0xffffffffu, lane != 0 || mbar_wait(empty0 + 8 * s, ph ^ 1, a.status));
+        if (!ok) break;
+        const int chunks = (nb + 63) / 64;  // dW: 64-wide boxes of dy
+        const int boxes = (nb + C::kBox - 1) / C::kBox;
+        const int tail = (left + 15) & ~15;
+        uint32_t bytes;
+        if constexpr (C::kGradW)
+          bytes = one_by_one ? tail * 128 * (2 + chunks) : kABytes + chunks * 8192;
+        else
+          bytes = kABytes + (a.rows != nullptr && !C::kMnA ? nb * 128 : boxes * C::kBox * 128);
+        if (lane == 0 && rank == 0) mbar_expect_tx(full0 + 8 * s, CTAS * bytes);
+        __syncwarp();
+        if constexpr (!C::kGradW) {
+          if (lane == 0) {
+            if constexpr (C::kGradX) {
+              for (int h = 0; h < 2; ++h)
+                load_3d<CTAS>(da + h * 8192, &maps.a, bar, i0 + 64 * h, k0, tl.id);
+            } else {
+              load_3d<CTAS>(da, &maps.a, bar, k0, i0, tl.id);
+            }
+          }
+          if (C::kGradX || a.rows == nullptr) {
+            if (lane == 0)
+              for (int q = 0; q < boxes; ++q)
+                load_2d<CTAS>(db + q * C::kBox * 128, &maps.b, bar, k0,
+                              tl.row0 + j0 + q * C::kBox);
+          } else if (4 * lane < nb) {
+            load_rows4<CTAS>(db + lane * 512, &maps.rows, bar, k0, idx);
+          }
+        } else if (!one_by_one) {
+          if (a.rows != nullptr) {
+            load_rows4<CTAS>(da + (lane >> 4) * 8192 + (lane & 15) * 512, &maps.rows, bar,
+                             i0 + 64 * (lane >> 4), idx);
+          } else if (lane < 2) {
+            load_2d<CTAS>(da + lane * 8192, &maps.a, bar, i0 + 64 * lane, tl.row0 + k0);
+          }
+          if (lane < chunks)
+            load_2d<CTAS>(db + lane * 8192, &maps.b, bar, j0 + 64 * lane, tl.row0 + k0);
+        } else {
+          // the last rows: each by itself, rows past the end from outside (zeros)
+          for (int r = lane; r < tail; r += 32) {
+            const bool in = r < left;
+            int xr = static_cast<int>(a.T);
+            if (in) xr = a.rows != nullptr ? token(tl.row0 + k0 + r, true) : tl.row0 + k0 + r;
+            const int yr = in ? tl.row0 + k0 + r : static_cast<int>(a.g.M);
+            for (int h = 0; h < 2; ++h)
+              load_2d<CTAS>(da + h * 8192 + r * 128, &maps.rows, bar, i0 + 64 * h, xr);
+            for (int h = 0; h < chunks; ++h)
+              load_2d<CTAS>(db + h * 8192 + r * 128, &maps.brow, bar, j0 + 64 * h, yr);
+          }
+        }
+        ++issued;
+        if (++s == stages) {
+          s = 0;
+          ph ^= 1;
+        }
+      }
+    }
+    timed_out = !ok;
+  } else if (warp == kEpiWarps + 1) {
+    // ---- products: one lane, of the pair's first CTA
+    if (lane == 0 && rank == 0) {
+      int s = 0;
+      uint32_t ph = 0, acc_no = 0;
+      bool ok = true;
+      for (int t = first; t < tiles && ok; t += step) {
+        const Tile tl = walk.at(t);
+        const uint32_t idesc =
+            (C::kI8 ? (2u << 4) : (1u << 4)) | (1u << 7) | (1u << 10) |
+            (C::kMnA ? 1u << 15 : 0u) | (C::kMnB ? 1u << 16 : 0u) |
+            (static_cast<uint32_t>(n_mma(tl) >> 3) << 17) |
+            (static_cast<uint32_t>(kBM * CTAS >> 4) << 24);
+        const int nk = (tl.K + C::kBlockK - 1) / C::kBlockK;
+        uint32_t acc = 0;
+        for (int kb = 0; kb < nk; ++kb) {
+          const bool starts = PIECES ? kb % kPieceBlocks == 0 : kb == 0;
+          const bool ends = kb == nk - 1 || (PIECES && (kb + 1) % kPieceBlocks == 0);
+          if (starts) {
+            const uint32_t b = acc_no & 1;
+            if (!mbar_wait(tempty0 + 8 * b, ((acc_no >> 1) & 1) ^ 1, a.status)) {
+              ok = false;
+              break;
+            }
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            acc = tmem + b * BN;
+          }
+          if (!mbar_wait(full0 + 8 * s, ph, a.status)) {
+            ok = false;
+            break;
+          }
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          const uint32_t da = sA + s * kABytes, db = sB + s * C::kBBytes;
+          const int left = tl.K - kb * C::kBlockK;
+          const int steps = left >= C::kBlockK ? C::kBlockK / C::kMmaK
+                                               : (left + C::kMmaK - 1) / C::kMmaK;
+#pragma unroll
+          for (int kk = 0; kk < C::kBlockK / C::kMmaK; ++kk) {
+            if (kk >= steps) break;
+            const uint64_t ad = C::kMnA ? mn_desc(da + kk * 2048) : sw128_desc(da + kk * 32);
+            const uint64_t bd = C::kMnB ? mn_desc(db + kk * 2048) : sw128_desc(db + kk * 32);
+            mma<CTAS, C::kI8>(acc, ad, bd, idesc, (starts && kk == 0) ? 0u : 1u);
+          }
+          commit<CTAS>(empty0 + 8 * s);
+          if (ends) {
+            commit<CTAS>(tfull0 + 8 * (acc_no & 1));
+            ++acc_no;
+          }
+          if (++s == stages) {
+            s = 0;
+            ph ^= 1;
+          }
+        }
+      }
+      timed_out = !ok;
+    }
+  } else {
+    // ---- results: TMEM lane = i, column = j; a warp takes 32 lanes and every
+    // other chunk of 32 columns
+    const int quarter = warp & 3, half = warp >> 2;
+    const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
+    uint32_t acc_no = 0;
+    bool ok = true;
+    for (int t = first; t < tiles && ok; t += step) {
+      const Tile tl = walk.at(t);
+      const int i = tl.i0 + rank * kBM + 32 * quarter + lane;
+      const int nk = (tl.K + C::kBlockK - 1) / C::kBlockK;
+      const int pieces = PIECES ? (nk + kPieceBlocks - 1) / kPieceBlocks : 1;
+      float ws = 0.0f;
+      if (C::kI8 && i < I) ws = a.Ws[static_cast<int64_t>(tl.id) * a.out + i];
+
+      auto wait_full = [&]() -> bool {
+        const bool got =
+            __all_sync(0xffffffffu, mbar_wait(tfull0 + 8 * (acc_no & 1), (acc_no >> 1) & 1, a.status));
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        return got;
+      };
+      auto drained = [&]() {  // this warp has read its part of the accumulator
+        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+          const uint32_t bar = tempty0 + 8 * (acc_no & 1);
+          if (CTAS == 2)
+            asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                             leader_addr(bar))
+                         : "memory");
+          else
+            mbar_arrive(bar);
+        }
+        ++acc_no;
+      };
+      // columns c .. c + 31 of this lane's i
+      auto store = [&](int c, const float* v) {
+        const int n = tl.n - c;  // columns that exist
+        if constexpr (C::kGradW) {
+          float* o = static_cast<float*>(a.o) + (static_cast<int64_t>(tl.id) * a.out + tl.j0 + c) * a.in + i;
+          if (i < I) {
+            if (a.accumulate) {
+#pragma unroll
+              for (int q = 0; q < 32; ++q)
+                if (q < n) o[static_cast<int64_t>(q) * a.in] += v[q];
+            } else {
+#pragma unroll
+              for (int q = 0; q < 32; ++q)
+                if (q < n) o[static_cast<int64_t>(q) * a.in] = v[q];
+            }
+          }
+        } else {
+          const int64_t at = static_cast<int64_t>(tl.row0 + tl.j0 + c) * I;
+          float z[32];
+          float xs = 0.0f;
+          if (C::kI8 && lane < n) {
+            const int r = tl.row0 + tl.j0 + c + lane;
+            int xr = r;
+            if (a.rows != nullptr) {
+              xr = a.rows[r];
+              if (xr < 0 || xr >= a.T) xr = 0;
+            }
+            xs = a.xs[xr];
+          }
+#pragma unroll
+          for (int q = 0; q < 32; ++q) {
+            z[q] = v[q];
+            if constexpr (C::kI8)
+              z[q] = static_cast<float>(__float_as_int(v[q])) *
+                     __shfl_sync(0xffffffffu, xs, q) * ws;
+            if (a.silu) z[q] = silu(z[q]);
+          }
+          if (a.out_f32) {
+            float* o = static_cast<float*>(a.o) + at + i;
+            if (i < I) {
+#pragma unroll
+              for (int q = 0; q < 32; ++q)
+                if (q < n) o[static_cast<int64_t>(q) * I] = z[q];
+            }
+          } else {
+            // two lanes trade so that each stores two neighbours of one column
+            const bool odd = lane & 1;
+            __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.o) + at + (i & ~1);
+#pragma unroll
+            for (int q = 0; q < 32; q += 2) {
+              const float got = __shfl_xor_sync(0xffffffffu, odd ? z[q] : z[q + 1], 1);
+              const __nv_bfloat162 w =
+                  odd ? __floats2bfloat162_rn(got, z[q + 1]) : __floats2bfloat162_rn(z[q], got);
+              if (i < I && q + (odd ? 1 : 0) < n)
+                *reinterpret_cast<__nv_bfloat162*>(o + static_cast<int64_t>(q + (odd ? 1 : 0)) * I) = w;
+            }
+          }
+        }
+      };
+
+      if constexpr (PIECES) {
+        constexpr int kAcc = BN > 32 ? BN / 2 : 32;  // columns of this warp
+        float sum[kAcc];
+#pragma unroll
+        for (int q = 0; q < kAcc; ++q) sum[q] = 0.0f;
+        for (int p = 0; p < pieces && ok; ++p) {
+          ok = wait_full();
+          if (!ok) break;
+#pragma unroll
+          for (int u = 0; u < kAcc / 32; ++u) {
+            const int c = (2 * u + half) * 32;
+            if (c < tl.n) {
+              uint32_t v[32];
+              tmem_ld32(tmem + lanes + (acc_no & 1) * BN + c, v);
+#pragma unroll
+              for (int q = 0; q < 32; ++q) sum[u * 32 + q] += __uint_as_float(v[q]);
+            }
+          }
+          drained();
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int u = 0; u < kAcc / 32; ++u) {
+          const int c = (2 * u + half) * 32;
+          if (c < tl.n) store(c, sum + u * 32);
+        }
+      } else {
+        ok = wait_full();
+        if (!ok) break;
+        for (int c = half * 32; c < tl.n; c += 64) {
+          uint32_t v[32];
+          tmem_ld32(tmem + lanes + (acc_no & 1) * BN + c, v);
+          store(c, reinterpret_cast<const float*>(v));
+        }
+        drained();
+      }
+    }
+    timed_out = !ok;
+  }
+  if (timed_out) aborted = 1u;
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  if (aborted != 0u) {
+    // a wait timed out: the loads and MMAs still in flight land (each wait
+    // bounded again) before TMEM is freed and the CTA exits
+    if (warp == kEpiWarps && lane == 0 && rank == 0) {
+      const uint32_t n = issued > static_cast<uint32_t>(stages) ? issued - stages : 0u;
+      for (uint32_t k = n; k < issued; ++k)
+        mbar_wait(full0 + 8 * (k % stages), (k / stages) & 1, a.status);
+    } else if (warp == kEpiWarps + 1 && lane == 0 && rank == 0) {
+      if (CTAS == 1) umma_commit(drain);
+      else commit<CTAS>(drain);
+      mbar_wait(drain, 0, a.status);
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncwarp();
+  }
+  // a pair's CTAs read each other's shared memory and barriers to the end
+  if (CTAS == 2) cluster_sync();
+  else __syncthreads();
+  pdl_trigger();
+  if (warp == kEpiWarps + 1) {
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    tmem_free<CTAS>(tmem, C::kCols);
+  }
+}
+
+// ---- host --------------------------------------------------------------------------
+
+// A tensor map of bytes-wide elements: dims innermost first, packed.
+bool make_map_nd(CUtensorMap* m, const void* base, bool i8, int nd, const int64_t* dim,
+                 const int* box) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  cuuint64_t d[3], st[2];
+  cuuint32_t bx[3], es[3] = {1, 1, 1};
+  int64_t bytes = i8 ? 1 : 2;
+  for (int q = 0; q < nd; ++q) {
+    d[q] = static_cast<cuuint64_t>(dim[q]);
+    bx[q] = static_cast<cuuint32_t>(box[q]);
+    bytes *= dim[q];
+    if (q + 1 < nd) st[q] = static_cast<cuuint64_t>(bytes);
+  }
+  return fn(m, i8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, nd,
+            const_cast<void*>(base), d, st, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <Product P, int CTAS, int BN, bool PIECES>
+cudaError_t launch(const LinearArgs& a, cudaStream_t s) {
+  using C = Cfg<P, CTAS, BN, PIECES>;
+  Maps m{};
+  const int64_t W[3] = {a.in, a.out, a.g.E}, X[2] = {a.in, a.T}, Y[2] = {a.out, a.g.M};
+  const int kb = C::kBlockK;
+  const int box_w[3] = {kb, C::kMnA ? 64 : kBM, 1}, box_r[2] = {kb, C::kBox};
+  const int box_64[2] = {64, 64}, box_1[2] = {kb, 1};
+  bool ok = true;
+  if (a.g.M > 0) {
+    if (C::kGradW) {
+      ok = make_map_nd(&m.a, a.x, false, 2, X, box_64) &&
+           make_map_nd(&m.b, a.dy, false, 2, Y, box_64) &&
+           make_map_nd(&m.rows, a.x, false, 2, X, box_1) &&
+           make_map_nd(&m.brow, a.dy, false, 2, Y, box_1);
+    } else {
+      ok = make_map_nd(&m.a, a.W, C::kI8, 3, W, box_w);
+      if (C::kGradX) ok = ok && make_map_nd(&m.b, a.dy, false, 2, Y, box_r);
+      else if (a.rows == nullptr) ok = ok && make_map_nd(&m.b, a.x, C::kI8, 2, X, box_r);
+      else ok = ok && make_map_nd(&m.rows, a.x, C::kI8, 2, X, box_1);
+    }
+  }
+  if (!ok) return cudaErrorInvalidValue;
+  int dev = 0, sms = 148;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const size_t fixed = 1024 + sizeof(GroupTab) * static_cast<size_t>(a.g.G);
+  const size_t statics = sizeof(GroupScratch) + (2 * kMaxStages + 5) * 8 + 64;
+  int stages = static_cast<int>((kSmemLimit - statics - fixed) / C::kStage);
+  if (stages > kMaxStages) stages = kMaxStages;
+  const size_t smem = fixed + static_cast<size_t>(stages) * C::kStage;
+  auto kernel = k_linear_tc<P, CTAS, BN, PIECES>;
+  OMNI_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(smem)));
+  // no more pairs (or CTAs) than there can be tiles
+  const int64_t mt = ((C::kMnA ? a.in : a.out) + kBM * CTAS - 1) / (kBM * CTAS);
+  const int64_t live = a.g.G < a.g.M ? a.g.G : a.g.M;
+  int64_t most = C::kGradW ? mt * ((a.out + BN - 1) / BN) * a.g.G : mt * (a.g.M / BN + live);
+  if (most > sms / CTAS) most = sms / CTAS;
+  if (most < 1) most = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(most * CTAS));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = CTAS;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = CTAS == 2 ? 2 : 1;
+  OMNI_TRY(cudaLaunchKernelEx(&cfg, kernel, m, a, stages));
+  return cudaGetLastError();
+}
+
+template <Product P, bool PIECES>
+cudaError_t pick(const LinearArgs& a, cudaStream_t s) {
+  return launch<P, 1, 128, PIECES>(a, s);
+}
+
+}  // namespace
+
+cudaError_t launch_linear(Product p, const LinearArgs& a, cudaStream_t s) {
+  if (encode_fn() == nullptr) return cudaErrorNotSupported;
+  const bool f32 = a.out_f32 != 0;
+  switch (p) {
+    case Product::kForward:
+      return f32 ? pick<Product::kForward, true>(a, s) : pick<Product::kForward, false>(a, s);
+    case Product::kGradX:
+      return f32 ? pick<Product::kGradX, true>(a, s) : pick<Product::kGradX, false>(a, s);
+    case Product::kGradW: return launch<Product::kGradW, 1, 128, true>(a, s);
+    default: return pick<Product::kInt8, false>(a, s);
+  }
+}
+
+}  // namespace omni
