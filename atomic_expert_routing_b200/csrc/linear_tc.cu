@@ -10,16 +10,19 @@
 // which is as wide as the group's rows need in steps of 16 per CTA.  A group
 // that ends inside a tile then costs no idle products, and a decode batch's
 // few rows per expert are an MMA of N = 16 or 32 over the streamed weights.
-// Rows past a group's end that a load brings along only reach columns that
-// are not stored; dW, whose sum runs over the rows, loads its last rows one
-// by one and reads zeros behind them.
 //
 // Operands come by TMA in 128-byte-swizzled tiles of 128 bytes of k (K-major)
-// or of 64 x 64 (the transposed operands of dx and dW, MN-major), rows by
-// token with gather4.  CTAS = 2 pairs two CTAs on one 256-wide tile: each
-// holds its half of A and of B, and the pair's first CTA issues the MMAs.
-// Warps 0-7 drain the accumulators, warp 8 loads, warp 9 issues; two TMEM
-// accumulators alternate, so a tile is stored while the next is summed.
+// or of 64 x 64 (the transposed operands of dx and dW, MN-major); rows of x
+// taken by token come by cp.async from two warps (a TMA row gather costs
+// about 77 cycles per four rows of 128 bytes, five times the products of the
+// tile they feed).  Rows past a group's end that a load brings along only
+// reach columns that are not stored; dW, whose sum runs over the rows, zeroes
+// the last block's in shared memory before its products.
+// CTAS = 2 pairs two CTAs on one 256-wide tile: each holds its half of A and
+// of B, and the pair's first CTA issues the MMAs.
+// Warps 0-7 drain the accumulators, warp 8 issues the TMA loads, warp 9 the
+// MMAs, warps 10-11 gather; two TMEM accumulators alternate, so a tile is
+// stored while the next is summed.
 //
 // PIECES: the tensor core's fp32 sums cut every addition towards zero, an
 // error of about 1.1e-9 of the result per term of k.  bf16 results do not
@@ -37,7 +40,9 @@ constexpr int kBM = 128;            // i per CTA
 constexpr int kABytes = kBM * 128;  // a stage's A tile: 128 bytes of k per row
 constexpr int kMaxStages = 12;
 constexpr int kEpiWarps = 8;
-constexpr int kThreads = 32 * (kEpiWarps + 2);
+constexpr int kLoadWarp = kEpiWarps, kMmaWarp = kEpiWarps + 1, kRowWarp = kEpiWarps + 2;
+constexpr int kRowWarps = 2, kRowThreads = 32 * kRowWarps;
+constexpr int kThreads = 32 * (kEpiWarps + 2 + kRowWarps);
 constexpr int kPieceBlocks = 8;     // k-blocks of 64 in a piece
 constexpr size_t kSmemLimit = 227 * 1024;
 
@@ -91,23 +96,19 @@ __device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap* m, uint
         "r"(c1), "r"(c2)
         : "memory");
 }
-// four rows r of a map whose box is one row high
-template <int CTAS>
-__device__ __forceinline__ void load_rows4(uint32_t dst, const CUtensorMap* m, uint32_t bar,
-                                           int c0, const int* r) {
-  if constexpr (CTAS == 1)
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4"
-        ".mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
-        "l"(m), "r"(bar), "r"(c0), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
-        : "memory");
-  else
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4"
-        ".mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(
-            dst),
-        "l"(m), "r"(bar), "r"(c0), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
-        : "memory");
+// 16 bytes from global to shared memory, zeros without `valid`
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(valid ? 16 : 0)
+               : "memory");
+}
+// arrive on bar (one of its expected arrivals) when this thread's copies so far have landed
+__device__ __forceinline__ void copies_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+// arrive on an mbarrier of either CTA of a pair
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 template <int CTAS, bool I8>
@@ -167,21 +168,84 @@ __device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
                  : "memory");
 }
 
-// Shared-memory descriptor of an MN-major tile with 128-byte swizzle: 64 of
-// the operand's M or N (128 bytes) per k, 8-k groups 1024 bytes apart, chunks
-// of 64 along M or N one [64 k x 128 bytes] box, 8192 bytes, apart.
-__device__ __forceinline__ uint64_t mn_desc(uint32_t saddr) {
-  return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) |
-         (static_cast<uint64_t>(8192 >> 4) << 16) | (static_cast<uint64_t>(1024 >> 4) << 32) |
-         (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
+// SiLU for a bf16 result: the fast exponential and reciprocal are off by at
+// most 2^-17 of the result (the rounding of z / ln 2, |z| < 89), where the
+// rounding to bf16 that follows is off by up to 2^-8.
+__device__ __forceinline__ float silu_fast(float z) {
+  float r;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.0f + __expf(-z)));
+  return z * r;
+}
+
+__device__ __forceinline__ void zero16(uint32_t dst) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst), "r"(0) : "memory");
+}
+
+// mbar_wait by a whole warp, for barriers that the other CTA of a pair
+// arrives on too; the outcome is the same in every lane
+__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+template <int CTAS>
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, int32_t* status) {
+  if (CTAS == 1) return __all_sync(0xffffffffu, mbar_wait(bar, parity, status));
+  if (__all_sync(0xffffffffu, try_wait_cluster(bar, parity))) return true;
+  const uint64_t t0 = global_ns();
+  for (uint32_t polls = 1;; ++polls) {
+    const bool got = try_wait_cluster(bar, parity);
+    if (__all_sync(0xffffffffu, got)) return true;
+    if (__any_sync(0xffffffffu, polls >= kWaitMaxPolls || global_ns() - t0 > kWaitLimitNs)) {
+      raise_status(status, OMNI_DEV_TIMEOUT);
+      return false;
+    }
+  }
+}
+
+// One lane of a converged warp.  tcgen05 and TMA instructions take their
+// operands from uniform registers: behind elect.sync the compiler knows that
+// one lane is left and issues them straight, behind `lane == 0` it wraps
+// each in a loop over the lanes (610 cycles per stage for four MMAs).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+// Shared-memory descriptors without their start address.  Of a K-major tile
+// with 128-byte swizzle: rows of 128 bytes, 8-row groups 1024 bytes apart.
+constexpr uint64_t kDescK = (1ull << 16) | (1024ull >> 4 << 32) | (1ull << 46) | (2ull << 61);
+// Of an MN-major tile with 128-byte swizzle: 64 of the operand's M or N (128
+// bytes) per k, 8-k groups 1024 bytes apart, chunks of 64 along M or N one
+// [64 k x 128 bytes] box, 8192 bytes, apart.
+constexpr uint64_t kDescMn =
+    (8192ull >> 4 << 16) | (1024ull >> 4 << 32) | (1ull << 46) | (2ull << 61);
+
+// 16 columns of this warp's 32 lanes
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+        "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
 // ---- the kernel ------------------------------------------------------------------
 
 struct Maps {
-  CUtensorMap a, b;  // boxes of an operand's tile (a: W, or x for dW)
-  CUtensorMap rows;  // x's rows one by one (gathered, or the last of dW)
-  CUtensorMap brow;  // dy's rows one by one (the last of dW)
+  CUtensorMap a, b;  // boxes of the two operands (a: W, or x for dW)
 };
 
 template <Product P, int CTAS, int BN, bool PIECES>
@@ -192,7 +256,7 @@ struct Cfg {
   static constexpr int kBlockK = kI8 ? 128 : 64;  // k per stage
   static constexpr int kMmaK = kI8 ? 32 : 16;
   static constexpr int kNb = BN / CTAS;           // j per CTA
-  static constexpr int kBox = kNb < 32 ? kNb : 32;  // rows of one B load
+  static constexpr int kBox = kGradW ? 64 : kNb < 32 ? kNb : 32;  // j of one B load
   static constexpr int kBBytes = kNb * 128;
   static constexpr int kStage = kABytes + kBBytes;
   static constexpr int kCols = 2 * BN;            // TMEM columns
@@ -240,13 +304,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   GroupTab* tab = reinterpret_cast<GroupTab*>(smem + stages * C::kStage);
   const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * kMaxStages;
   const uint32_t tfull0 = empty0 + 8 * kMaxStages, tempty0 = tfull0 + 16, drain = tempty0 + 16;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int rank = CTAS == 2 ? static_cast<int>(cluster_rank()) : 0;
   const int first = blockIdx.x / CTAS, step = gridDim.x / CTAS;
 
+  const bool gathers = !C::kGradX && a.rows != nullptr;
+  // Where a half needs more than its TMA loads (gathered rows, rows to zero),
+  // each CTA of a pair waits for its own and the second tells the first;
+  // else the loads of both report to the first.
+  const bool halves = C::kGradW || gathers;
   if (threadIdx.x == 0) {
+    // a stage is full after its loads' expect, its gathered rows, and in a
+    // pair's first CTA the second's word that its half is ready
+    const int arrivals =
+        1 + (gathers ? kRowThreads : 0) + (halves && CTAS == 2 && rank == 0 ? 1 : 0);
     for (int s = 0; s < stages; ++s) {
-      mbar_init(full0 + 8 * s, 1);
+      mbar_init(full0 + 8 * s, arrivals);
       mbar_init(empty0 + 8 * s, 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -258,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
-  if (warp == kEpiWarps + 1) tmem_alloc<CTAS>(smem_u32(&tmem_slot), C::kCols);
+  if (warp == kMmaWarp) tmem_alloc<CTAS>(smem_u32(&tmem_slot), C::kCols);
   pdl_wait();
   const int I = C::kMnA ? a.in : a.out;
   const int mt = (I + kBM * CTAS - 1) / (kBM * CTAS);
@@ -279,97 +352,51 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto n_mma = [](const Tile& t) { return (t.n + 16 * CTAS - 1) / (16 * CTAS) * (16 * CTAS); };
 
   bool timed_out = false;
-  uint32_t issued = 0;  // stages loaded
-  if (warp == kEpiWarps) {
-    // ---- loads: lane 0, or every lane where rows are loaded one by one
+  uint32_t issued = 0;  // stages this thread has loaded
+  if (warp == kLoadWarp) {
+    // ---- TMA loads
     int s = 0;
     uint32_t ph = 0;
     bool ok = true;
-    // a row of x by its place in the group order, checked
-    auto token = [&](int r, bool valid) -> int {
-      if (!valid) return 0;
-      const int v = a.rows[r];
-      if (v >= 0 && v < a.T) return v;
-      raise_status(a.status, OMNI_DEV_BAD_INDEX);
-      return 0;
-    };
     for (int t = first; t < tiles && ok; t += step) {
       const Tile tl = walk.at(t);
       const int nb = n_mma(tl) / CTAS;  // j of this CTA: j0 + rank * nb ..
       const int i0 = tl.i0 + rank * kBM, j0 = tl.j0 + rank * nb;
       const int nk = (tl.K + C::kBlockK - 1) / C::kBlockK;
-      int idx[4] = {0, 0, 0, 0};
-      if (!C::kMnA && a.rows != nullptr) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          idx[q] = token(tl.row0 + j0 + 4 * lane + q, 4 * lane < nb && j0 + 4 * lane + q < tl.j0 + tl.n);
-      }
+      const int boxes = (nb + C::kBox - 1) / C::kBox;
+      const uint32_t a_bytes = C::kGradW && gathers ? 0 : kABytes;
+      const uint32_t b_bytes = !C::kGradW && gathers ? 0 : boxes * C::kBox * 128;
       for (int kb = 0; kb < nk; ++kb) {
-        const uint32_t bar = CTAS == 2 ? leader_addr(full0 + 8 * s) : full0 + 8 * s;
+        const uint32_t bar = CTAS == 2 && !halves ? leader_addr(full0 + 8 * s) : full0 + 8 * s;
         const uint32_t da = sA + s * kABytes, db = sB + s * C::kBBytes;
         const int k0 = kb * C::kBlockK;
-        const int left = tl.K - k0;
-        const bool one_by_one = C::kGradW && left < C::kBlockK;
-        if constexpr (C::kGradW) {
-          if (a.rows != nullptr) {  // the block's rows, read before its stage is free
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const int r = 4 * (lane & 15) + q;
-              idx[q] = token(tl.row0 + k0 + r, r < left);
-            }
-          }
-        }
-        ok = __all_sync(0xffffffffu, lane != 0 || mbar_wait(empty0 + 8 * s, ph ^ 1, a.status));
+        ok = __all_sync(0xffffffffu, mbar_wait(empty0 + 8 * s, ph ^ 1, a.status));
         if (!ok) break;
-        const int chunks = (nb + 63) / 64;  // dW: 64-wide boxes of dy
-        const int boxes = (nb + C::kBox - 1) / C::kBox;
-        const int tail = (left + 15) & ~15;
-        uint32_t bytes;
-        if constexpr (C::kGradW)
-          bytes = one_by_one ? tail * 128 * (2 + chunks) : kABytes + chunks * 8192;
-        else
-          bytes = kABytes + (a.rows != nullptr && !C::kMnA ? nb * 128 : boxes * C::kBox * 128);
-        if (lane == 0 && rank == 0) mbar_expect_tx(full0 + 8 * s, CTAS * bytes);
-        __syncwarp();
-        if constexpr (!C::kGradW) {
-          if (lane == 0) {
+        if (elect_one()) {
+          if (halves)
+            mbar_expect_tx(full0 + 8 * s, a_bytes + b_bytes);
+          else if (rank == 0)
+            mbar_expect_tx(full0 + 8 * s, CTAS * (a_bytes + b_bytes));
+          if constexpr (C::kGradW) {
+            if (!gathers)
+              for (int h = 0; h < 2; ++h)
+                load_2d<1>(da + h * 8192, &maps.a, bar, i0 + 64 * h, tl.row0 + k0);
+            for (int h = 0; h < boxes; ++h)
+              load_2d<1>(db + h * 8192, &maps.b, bar, j0 + 64 * h, tl.row0 + k0);
+          } else {
             if constexpr (C::kGradX) {
               for (int h = 0; h < 2; ++h)
                 load_3d<CTAS>(da + h * 8192, &maps.a, bar, i0 + 64 * h, k0, tl.id);
             } else {
               load_3d<CTAS>(da, &maps.a, bar, k0, i0, tl.id);
             }
-          }
-          if (C::kGradX || a.rows == nullptr) {
-            if (lane == 0)
+            if (!gathers)
               for (int q = 0; q < boxes; ++q)
                 load_2d<CTAS>(db + q * C::kBox * 128, &maps.b, bar, k0,
                               tl.row0 + j0 + q * C::kBox);
-          } else if (4 * lane < nb) {
-            load_rows4<CTAS>(db + lane * 512, &maps.rows, bar, k0, idx);
-          }
-        } else if (!one_by_one) {
-          if (a.rows != nullptr) {
-            load_rows4<CTAS>(da + (lane >> 4) * 8192 + (lane & 15) * 512, &maps.rows, bar,
-                             i0 + 64 * (lane >> 4), idx);
-          } else if (lane < 2) {
-            load_2d<CTAS>(da + lane * 8192, &maps.a, bar, i0 + 64 * lane, tl.row0 + k0);
-          }
-          if (lane < chunks)
-            load_2d<CTAS>(db + lane * 8192, &maps.b, bar, j0 + 64 * lane, tl.row0 + k0);
-        } else {
-          // the last rows: each by itself, rows past the end from outside (zeros)
-          for (int r = lane; r < tail; r += 32) {
-            const bool in = r < left;
-            int xr = static_cast<int>(a.T);
-            if (in) xr = a.rows != nullptr ? token(tl.row0 + k0 + r, true) : tl.row0 + k0 + r;
-            const int yr = in ? tl.row0 + k0 + r : static_cast<int>(a.g.M);
-            for (int h = 0; h < 2; ++h)
-              load_2d<CTAS>(da + h * 8192 + r * 128, &maps.rows, bar, i0 + 64 * h, xr);
-            for (int h = 0; h < chunks; ++h)
-              load_2d<CTAS>(db + h * 8192 + r * 128, &maps.brow, bar, j0 + 64 * h, yr);
           }
         }
+        __syncwarp();
         ++issued;
         if (++s == stages) {
           s = 0;
@@ -378,9 +405,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     timed_out = !ok;
-  } else if (warp == kEpiWarps + 1) {
-    // ---- products: one lane, of the pair's first CTA
-    if (lane == 0 && rank == 0) {
+  } else if (warp == kMmaWarp) {
+    // ---- products: issued by one lane of the pair's first CTA
+    if (rank == 0 || halves) {
       int s = 0;
       uint32_t ph = 0, acc_no = 0;
       bool ok = true;
@@ -396,42 +423,150 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int kb = 0; kb < nk; ++kb) {
           const bool starts = PIECES ? kb % kPieceBlocks == 0 : kb == 0;
           const bool ends = kb == nk - 1 || (PIECES && (kb + 1) % kPieceBlocks == 0);
-          if (starts) {
+          if (starts && rank == 0) {
             const uint32_t b = acc_no & 1;
-            if (!mbar_wait(tempty0 + 8 * b, ((acc_no >> 1) & 1) ^ 1, a.status)) {
-              ok = false;
-              break;
-            }
+            ok = wait_warp<CTAS>(tempty0 + 8 * b, ((acc_no >> 1) & 1) ^ 1, a.status);
+            if (!ok) break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             acc = tmem + b * BN;
           }
-          if (!mbar_wait(full0 + 8 * s, ph, a.status)) {
-            ok = false;
-            break;
-          }
-          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
           const uint32_t da = sA + s * kABytes, db = sB + s * C::kBBytes;
           const int left = tl.K - kb * C::kBlockK;
-          const int steps = left >= C::kBlockK ? C::kBlockK / C::kMmaK
-                                               : (left + C::kMmaK - 1) / C::kMmaK;
+          ok = wait_warp<CTAS>(full0 + 8 * s, ph, a.status);
+          if (!ok) break;
+          if constexpr (C::kGradW) {
+            // rows past the group's end, up to the last product's 16: zeros (of
+            // both operands: what is there may be infinite).  The second CTA
+            // says when its half is ready.
+            if (left < C::kBlockK && (left & 15) != 0) {
+              const int rows = 16 - (left & 15), nb = n_mma(tl) / CTAS;
+              for (int g = lane; g < rows * 8; g += 32) {
+                const uint32_t at = (left + (g >> 3)) * 128 + (g & 7) * 16;
+                if (!gathers)
+                  for (int h = 0; h < 2; ++h) zero16(da + h * 8192 + at);
+                for (int h = 0; h < (nb + 63) / 64; ++h) zero16(db + h * 8192 + at);
+              }
+              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            }
+          }
+          // rows copied by threads, before the tensor core reads them
+          if (gathers) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          if (CTAS == 2 && halves) {
+            __syncwarp();
+            if (rank != 0 && lane == 0) arrive_cluster(leader_addr(full0 + 8 * s));
+          }
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          if (rank == 0 && elect_one()) {
+            const int steps = left >= C::kBlockK ? C::kBlockK / C::kMmaK
+                                                 : (left + C::kMmaK - 1) / C::kMmaK;
+            const uint64_t ad = (C::kMnA ? kDescMn : kDescK) | (da >> 4);
+            const uint64_t bd = (C::kMnB ? kDescMn : kDescK) | (db >> 4);
+            // a step of k: 32 bytes along K-major rows, 16 rows of an MN-major tile
+            constexpr int sa = (C::kMnA ? 2048 : 32) >> 4, sb = (C::kMnB ? 2048 : 32) >> 4;
+            mma<CTAS, C::kI8>(acc, ad, bd, idesc, starts ? 0u : 1u);
 #pragma unroll
-          for (int kk = 0; kk < C::kBlockK / C::kMmaK; ++kk) {
-            if (kk >= steps) break;
-            const uint64_t ad = C::kMnA ? mn_desc(da + kk * 2048) : sw128_desc(da + kk * 32);
-            const uint64_t bd = C::kMnB ? mn_desc(db + kk * 2048) : sw128_desc(db + kk * 32);
-            mma<CTAS, C::kI8>(acc, ad, bd, idesc, (starts && kk == 0) ? 0u : 1u);
+            for (int kk = 1; kk < C::kBlockK / C::kMmaK; ++kk)
+              if (kk < steps) mma<CTAS, C::kI8>(acc, ad + kk * sa, bd + kk * sb, idesc, 1u);
+            commit<CTAS>(empty0 + 8 * s);
+            if (ends) commit<CTAS>(tfull0 + 8 * (acc_no & 1));
           }
-          commit<CTAS>(empty0 + 8 * s);
-          if (ends) {
-            commit<CTAS>(tfull0 + 8 * (acc_no & 1));
-            ++acc_no;
-          }
+          __syncwarp();
+          if (ends) ++acc_no;
           if (++s == stages) {
             s = 0;
             ph ^= 1;
           }
         }
       }
+      timed_out = !ok;
+    }
+  } else if (warp >= kRowWarp) {
+    // ---- x's rows by token: 16 bytes a copy, eight copies to a row's 128 bytes
+    if (gathers) {
+      constexpr int kRows = C::kGradW ? 64 : C::kNb;         // of a stage
+      constexpr int kMine = (kRows + kRowThreads / 8 - 1) / (kRowThreads / 8);
+      const int tid = threadIdx.x - 32 * kRowWarp;
+      const int r0 = tid >> 3, piece = tid & 7;
+      const uint32_t place = static_cast<uint32_t>((piece ^ (r0 & 7)) * 16);  // swizzled
+      const int64_t pitch = static_cast<int64_t>(a.in) * (C::kI8 ? 1 : 2);
+      const char* x = static_cast<const char*>(a.x);
+      auto checked = [&](int v) -> int {  // a row number as the caller gave it
+        if (v >= 0 && v < a.T) return v;
+        raise_status(a.status, OMNI_DEV_BAD_INDEX);
+        return 0;
+      };
+      int s = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int t = first; t < tiles && ok; t += step) {
+        const Tile tl = walk.at(t);
+        const int nb = n_mma(tl) / CTAS;
+        const int nk = (tl.K + C::kBlockK - 1) / C::kBlockK;
+        const int i0 = tl.i0 + rank * kBM;
+        const int mine = tl.n - rank * nb;  // dW: unused; else rows of this CTA
+        const int row0 = C::kGradW ? tl.row0 : tl.row0 + tl.j0 + rank * nb;
+        // dW takes other rows every block: each lane reads two of the block's
+        // 64 row numbers, three blocks ahead
+        int2 ahead[3];
+        auto fetch = [&](int kb) -> int2 {
+          const int r = kb * 64 + lane;
+          return make_int2(r < tl.K ? a.rows[row0 + r] : -1,
+                           r + 32 < tl.K ? a.rows[row0 + r + 32] : -1);
+        };
+        int idx[kMine];
+        if constexpr (C::kGradW) {
+#pragma unroll
+          for (int q = 0; q < 3; ++q) ahead[q] = fetch(q);
+        } else {
+#pragma unroll
+          for (int q = 0; q < kMine; ++q) {
+            const int r = r0 + q * (kRowThreads / 8);
+            idx[q] = r < mine && r < kRows ? checked(a.rows[row0 + r]) : -1;
+          }
+        }
+        for (int kb = 0; kb < nk; ++kb) {
+          ok = __all_sync(0xffffffffu, mbar_wait(empty0 + 8 * s, ph ^ 1, a.status));
+          if (!ok) break;
+          if constexpr (C::kGradW) {
+            const int left = tl.K - kb * 64;
+            const int2 v = make_int2(lane < left ? checked(ahead[0].x) : -1,
+                                     lane + 32 < left ? checked(ahead[0].y) : -1);
+            ahead[0] = ahead[1];
+            ahead[1] = ahead[2];
+            ahead[2] = fetch(kb + 3);
+            const uint32_t da = sA + s * kABytes + r0 * 128 + place;
+            const int c = i0 + 8 * piece;
+            const char* xc = x + static_cast<int64_t>(c) * 2;
+#pragma unroll
+            for (int q = 0; q < kMine; ++q) {
+              const int r = r0 + q * (kRowThreads / 8);
+              const int row = __shfl_sync(0xffffffffu, q < kMine / 2 ? v.x : v.y, r & 31);
+              const char* p = xc + row * pitch;
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const bool in = row >= 0 && c + 64 * h < a.in;
+                copy16(da + h * 8192 + q * (kRowThreads / 8) * 128, in ? p + 128 * h : x, in);
+              }
+            }
+          } else {
+            const uint32_t db = sB + s * C::kBBytes + r0 * 128 + place;
+            const int64_t c = static_cast<int64_t>(kb) * 128 + 16 * piece;  // bytes
+            const bool wide = c < pitch;
+#pragma unroll
+            for (int q = 0; q < kMine; ++q) {
+              if (q * (kRowThreads / 8) >= nb) break;
+              const bool in = idx[q] >= 0 && wide;
+              copy16(db + q * (kRowThreads / 8) * 128, in ? x + idx[q] * pitch + c : x, in);
+            }
+          }
+          copies_arrive(full0 + 8 * s);
+          if (++s == stages) {
+            s = 0;
+            ph ^= 1;
+          }
+        }
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
       timed_out = !ok;
     }
   } else {
@@ -460,12 +595,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) {
           const uint32_t bar = tempty0 + 8 * (acc_no & 1);
-          if (CTAS == 2)
-            asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
-                             leader_addr(bar))
-                         : "memory");
-          else
-            mbar_arrive(bar);
+          if (CTAS == 2) arrive_cluster(leader_addr(bar));
+          else mbar_arrive(bar);
         }
         ++acc_no;
       };
@@ -504,7 +635,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             if constexpr (C::kI8)
               z[q] = static_cast<float>(__float_as_int(v[q])) *
                      __shfl_sync(0xffffffffu, xs, q) * ws;
-            if (a.silu) z[q] = silu(z[q]);
+          }
+          if (a.silu) {
+            if (a.out_f32) {
+#pragma unroll
+              for (int q = 0; q < 32; ++q) z[q] = silu(z[q]);
+            } else {
+#pragma unroll
+              for (int q = 0; q < 32; ++q) z[q] = silu_fast(z[q]);
+            }
           }
           if (a.out_f32) {
             float* o = static_cast<float*>(a.o) + at + i;
@@ -541,10 +680,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int u = 0; u < kAcc / 32; ++u) {
             const int c = (2 * u + half) * 32;
             if (c < tl.n) {
-              uint32_t v[32];
-              tmem_ld32(tmem + lanes + (acc_no & 1) * BN + c, v);
 #pragma unroll
-              for (int q = 0; q < 32; ++q) sum[u * 32 + q] += __uint_as_float(v[q]);
+              for (int w = 0; w < 32; w += 16) {
+                uint32_t v[16];
+                tmem_ld16(tmem + lanes + (acc_no & 1) * BN + c + w, v);
+#pragma unroll
+                for (int q = 0; q < 16; ++q) sum[u * 32 + w + q] += __uint_as_float(v[q]);
+              }
             }
           }
           drained();
@@ -574,11 +716,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (aborted != 0u) {
     // a wait timed out: the loads and MMAs still in flight land (each wait
     // bounded again) before TMEM is freed and the CTA exits
-    if (warp == kEpiWarps && lane == 0 && rank == 0) {
+    if (warp == kLoadWarp && lane == 0 && (rank == 0 || halves)) {
       const uint32_t n = issued > static_cast<uint32_t>(stages) ? issued - stages : 0u;
       for (uint32_t k = n; k < issued; ++k)
         mbar_wait(full0 + 8 * (k % stages), (k / stages) & 1, a.status);
-    } else if (warp == kEpiWarps + 1 && lane == 0 && rank == 0) {
+    } else if (warp == kMmaWarp && lane == 0 && rank == 0) {
       if (CTAS == 1) umma_commit(drain);
       else commit<CTAS>(drain);
       mbar_wait(drain, 0, a.status);
@@ -590,7 +732,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (CTAS == 2) cluster_sync();
   else __syncthreads();
   pdl_trigger();
-  if (warp == kEpiWarps + 1) {
+  if (warp == kMmaWarp) {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     tmem_free<CTAS>(tmem, C::kCols);
   }
@@ -625,19 +767,15 @@ cudaError_t launch(const LinearArgs& a, cudaStream_t s) {
   const int64_t W[3] = {a.in, a.out, a.g.E}, X[2] = {a.in, a.T}, Y[2] = {a.out, a.g.M};
   const int kb = C::kBlockK;
   const int box_w[3] = {kb, C::kMnA ? 64 : kBM, 1}, box_r[2] = {kb, C::kBox};
-  const int box_64[2] = {64, 64}, box_1[2] = {kb, 1};
+  const int box_64[2] = {64, 64};
   bool ok = true;
   if (a.g.M > 0) {
     if (C::kGradW) {
       ok = make_map_nd(&m.a, a.x, false, 2, X, box_64) &&
-           make_map_nd(&m.b, a.dy, false, 2, Y, box_64) &&
-           make_map_nd(&m.rows, a.x, false, 2, X, box_1) &&
-           make_map_nd(&m.brow, a.dy, false, 2, Y, box_1);
+           make_map_nd(&m.b, a.dy, false, 2, Y, box_64);
     } else {
-      ok = make_map_nd(&m.a, a.W, C::kI8, 3, W, box_w);
-      if (C::kGradX) ok = ok && make_map_nd(&m.b, a.dy, false, 2, Y, box_r);
-      else if (a.rows == nullptr) ok = ok && make_map_nd(&m.b, a.x, C::kI8, 2, X, box_r);
-      else ok = ok && make_map_nd(&m.rows, a.x, C::kI8, 2, X, box_1);
+      ok = make_map_nd(&m.a, a.W, C::kI8, 3, W, box_w) &&
+           make_map_nd(&m.b, C::kGradX ? a.dy : a.x, C::kI8, 2, C::kGradX ? Y : X, box_r);
     }
   }
   if (!ok) return cudaErrorInvalidValue;
@@ -678,7 +816,14 @@ cudaError_t launch(const LinearArgs& a, cudaStream_t s) {
 
 template <Product P, bool PIECES>
 cudaError_t pick(const LinearArgs& a, cudaStream_t s) {
-  return launch<P, 1, 128, PIECES>(a, s);
+  const int64_t live = a.g.G < a.g.M ? a.g.G : a.g.M;
+  const int64_t each = (a.g.M + live - 1) / live;  // rows of a group, on average
+  const int rule = each <= 32 ? 32 : each <= 64 ? 64 : each <= 128 ? 128 : 256;
+  int v = rule;
+  if (v == 32) return launch<P, 1, 32, PIECES>(a, s);
+  if (v == 64) return launch<P, 1, 64, PIECES>(a, s);
+  if (v == 128) return launch<P, 1, 128, PIECES>(a, s);
+  return launch<P, 2, 256, PIECES>(a, s);
 }
 
 }  // namespace
@@ -691,7 +836,8 @@ cudaError_t launch_linear(Product p, const LinearArgs& a, cudaStream_t s) {
       return f32 ? pick<Product::kForward, true>(a, s) : pick<Product::kForward, false>(a, s);
     case Product::kGradX:
       return f32 ? pick<Product::kGradX, true>(a, s) : pick<Product::kGradX, false>(a, s);
-    case Product::kGradW: return launch<Product::kGradW, 1, 128, true>(a, s);
+    case Product::kGradW:
+      return launch<Product::kGradW, 2, 256, true>(a, s);
     default: return pick<Product::kInt8, false>(a, s);
   }
 }
