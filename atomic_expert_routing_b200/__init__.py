@@ -499,54 +499,77 @@ _OUT = {torch.float32: OMNI_F32, torch.bfloat16: OMNI_BF16}
 
 
 def _out_code(name, dtype):
-    if dtype not in _OUT:
+    code = _OUT.get(dtype)
+    if code is None:
         raise ValueError(f"{name}: dtype {dtype}, the call writes float32 or bfloat16")
-    return _OUT[dtype]
+    return code
 
 
-def _linear_setup(x, W, group_off, ids, n_groups, rows, dtype, others, names=("x", "W")):
-    """The checks the grouped products share; (dims, device) of a call of
+def _address(name, t, dev):
+    """A tensor's address for the library (None: no tensor).  The calls below
+    are short enough that the binding's own time counts: plain integers."""
+    if t is None:
+        return None
+    if t.device != dev:
+        raise ValueError(f"{name}: on {t.device}, the call's first tensor is on {dev}")
+    if not t.is_cuda:
+        raise ValueError("tensors passed to the CUDA library must live on a CUDA device")
+    if not t.is_contiguous():
+        raise ValueError("tensors passed to the CUDA library must be contiguous")
+    return t.data_ptr()
+
+
+def _linear_dims(names, x, W, group_off, ids, n_groups, rows, counts, dtype):
+    """The checks the grouped products share, and the dims of a call of
     x [T, in] with W [E, out, in] of the given dtype."""
     i32 = torch.int32
-    for name, t, nd in ((names[0], x, 2), (names[1], W, 3)):
-        if t.dtype != dtype:
-            raise ValueError(f"{name}: dtype {t.dtype}, the call reads {dtype}")
-        if t.dim() != nd:
-            raise ValueError(f"{name}: {t.dim()} dimensions, the call reads {nd}")
-    if x.shape[1] != W.shape[2]:
-        raise ValueError(f"{names[0]}: rows of {x.shape[1]} elements, {names[1]} takes "
-                         f"{W.shape[2]}")
-    dev = x.device
-    G = 1 if group_off is None else group_off.numel() - 1
+    if x.dtype != dtype:
+        raise ValueError(f"{names[0]}: dtype {x.dtype}, the call reads {dtype}")
+    if W.dtype != dtype:
+        raise ValueError(f"{names[1]}: dtype {W.dtype}, the call reads {dtype}")
+    if x.dim() != 2:
+        raise ValueError(f"{names[0]}: {x.dim()} dimensions, the call reads 2")
+    if W.dim() != 3:
+        raise ValueError(f"{names[1]}: {W.dim()} dimensions, the call reads 3")
+    T, n_in = x.shape
+    E, n_out, w_in = W.shape
+    if n_in != w_in:
+        raise ValueError(f"{names[0]}: rows of {n_in} elements, {names[1]} takes {w_in}")
+    G = 1
     if group_off is not None:
         _expect("group_off", group_off, 2, i32)
-    _expect("ids", ids, G, i32, optional=True)
-    _expect("n_groups", n_groups, 1, i32, optional=True)
-    _expect("rows", rows, 0, i32, optional=True)
-    for name, t in ((names[1], W), ("group_off", group_off), ("ids", ids),
-                    ("n_groups", n_groups), ("rows", rows), *others):
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name}: on {t.device}, {names[0]} is on {dev}")
-    M = x.shape[0] if rows is None else rows.numel()
-    return _lib.LinearDims(M, x.shape[0], x.shape[1], W.shape[1], W.shape[0], G), dev
+        G = group_off.numel() - 1
+    if ids is not None:
+        _expect("ids", ids, G, i32)
+    if n_groups is not None:
+        _expect("n_groups", n_groups, 1, i32)
+    if rows is not None:
+        _expect("rows", rows, 0, i32)
+    if counts is not None:
+        _expect("counts", counts, 4, i32)
+    return _lib.LinearDims(T if rows is None else rows.numel(), T, n_in, n_out, E, G)
 
 
-def _on(dev, stream, fn, args):
-    """Run a library call with dev current, on stream (default: dev's current one)."""
-    with torch.cuda.device(dev):
-        s = torch.cuda.current_stream(dev) if stream is None else stream
-        _lib.check(fn, getattr(_lib.load(), fn)(*args, C.c_void_p(s.cuda_stream)))
+def _run(fn, dev, stream, *args):
+    """A library call on stream (default: the current one of dev), with dev current."""
+    lib = _lib.load()
+    s = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == dev.index:
+        code = getattr(lib, fn)(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            code = getattr(lib, fn)(*args, s)
+    _lib.check(fn, code)
 
 
-def _linear_out(name, t, M, width, dtype, dev):
+def _linear_out(name, t, like, M, width, dtype):
     """The output [M, width]: t if given (its dtype is the call's), else a new
-    tensor of dtype."""
+    tensor of dtype beside like; and its dtype's code."""
     if t is None:
-        _out_code("out_dtype", dtype)
-        return torch.empty((M, width), dtype=dtype, device=dev)
-    _out_code(name, t.dtype)
+        return like.new_empty((M, width), dtype=dtype), _out_code("out_dtype", dtype)
+    code = _out_code(name, t.dtype)
     _expect(name, t, M * width, t.dtype)
-    return t
+    return t, code
 
 
 def grouped_linear(x, W, group_off, *, ids=None, n_groups=None, rows=None, silu=False, y=None,
@@ -558,14 +581,15 @@ def grouped_linear(x, W, group_off, *, ids=None, n_groups=None, rows=None, silu=
     A schedule with B = 1 has them: group_off, uniq, counts[1:2] and task_token.  Returns
     y [M, out] in out_dtype (bf16 or fp32; of the given y, its own); rows in no group are
     left as they were."""
-    D, dev = _linear_setup(x, W, group_off, ids, n_groups, rows, torch.bfloat16,
-                           (("y", y), ("counts", counts)))
-    _expect("counts", counts, 4, torch.int32, optional=True)
-    y = _linear_out("y", y, D.M, D.out, out_dtype, dev)
-    D.out_dtype, D.flags = _out_code("y", y.dtype), OMNI_LINEAR_SILU if silu else 0
-    _on(dev, stream, "omni_grouped_linear",
-        (C.byref(D), _ptr(x), _ptr(W), _ptr(group_off), _ptr(ids), _ptr(n_groups), _ptr(rows),
-         _ptr(y), _ptr(counts)))
+    D = _linear_dims(("x", "W"), x, W, group_off, ids, n_groups, rows, counts, torch.bfloat16)
+    dev = x.device
+    y, D.out_dtype = _linear_out("y", y, x, D.M, D.out, out_dtype)
+    if silu:
+        D.flags = OMNI_LINEAR_SILU
+    _run("omni_grouped_linear", dev, stream, C.byref(D), _address("x", x, dev),
+         _address("W", W, dev), _address("group_off", group_off, dev), _address("ids", ids, dev),
+         _address("n_groups", n_groups, dev), _address("rows", rows, dev),
+         _address("y", y, dev), _address("counts", counts, dev))
     return y
 
 
@@ -578,16 +602,14 @@ def grouped_linear_backward(x, W, dy, group_off, *, ids=None, n_groups=None, row
     dW [E, out, in] fp32.  A given dW is added to (accumulate) or overwritten (the matrices of
     no group are left as they were either way); without one, a new dW holds zeros there.
     Returns a dict of those asked for."""
-    D, dev = _linear_setup(x, W, group_off, ids, n_groups, rows, torch.bfloat16,
-                           (("dy", dy), ("dx", dx), ("dW", dW), ("counts", counts)))
+    D = _linear_dims(("x", "W"), x, W, group_off, ids, n_groups, rows, counts, torch.bfloat16)
+    dev = x.device
     _expect("dy", dy, D.M * D.out, torch.bfloat16)
-    _expect("counts", counts, 4, torch.int32, optional=True)
     if not (need_dx or need_dW):
         raise ValueError("need_dx and need_dW: no gradient asked for")
     g = {}
     if need_dx:
-        g["dx"] = _linear_out("dx", dx, D.M, D.in_, out_dtype, dev)
-        D.out_dtype = _out_code("dx", g["dx"].dtype)
+        g["dx"], D.out_dtype = _linear_out("dx", dx, x, D.M, D.in_, out_dtype)
     if need_dW:
         if dW is None:
             # with ids or n_groups some matrices may be in no group
@@ -597,10 +619,12 @@ def grouped_linear_backward(x, W, dy, group_off, *, ids=None, n_groups=None, row
         else:
             _expect("dW", dW, W.numel(), torch.float32)
             g["dW"] = dW
-    _on(dev, stream, "omni_grouped_linear_backward",
-        (C.byref(D), _ptr(x), _ptr(W), _ptr(dy), _ptr(group_off), _ptr(ids), _ptr(n_groups),
-         _ptr(rows), _ptr(g.get("dx")), _ptr(g.get("dW")), 1 if accumulate else 0,
-         _ptr(counts)))
+    _run("omni_grouped_linear_backward", dev, stream, C.byref(D), _address("x", x, dev),
+         _address("W", W, dev), _address("dy", dy, dev), _address("group_off", group_off, dev),
+         _address("ids", ids, dev), _address("n_groups", n_groups, dev),
+         _address("rows", rows, dev), _address("dx", g.get("dx"), dev),
+         _address("dW", g.get("dW"), dev), 1 if accumulate else 0,
+         _address("counts", counts, dev))
     return g
 
 
@@ -617,14 +641,12 @@ def quantize_rows(x, *, q=None, scale=None, stream=None):
     _expect("q", q, x.numel(), torch.int8, optional=True)
     _expect("scale", scale, n, torch.float32, optional=True)
     dev = x.device
-    for name, t in (("q", q), ("scale", scale)):
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name}: on {t.device}, x is on {dev}")
     if q is None:
-        q = torch.empty(x.shape, dtype=torch.int8, device=dev)
+        q = torch.empty_like(x, dtype=torch.int8, memory_format=torch.contiguous_format)
     if scale is None:
-        scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
-    _on(dev, stream, "omni_quantize_rows", (n, width, code, _ptr(x), _ptr(q), _ptr(scale)))
+        scale = x.new_empty(x.shape[:-1], dtype=torch.float32)
+    _run("omni_quantize_rows", dev, stream, n, width, code, _address("x", x, dev),
+         _address("q", q, dev), _address("scale", scale, dev))
     return q, scale
 
 
@@ -641,17 +663,18 @@ def quantized_linear(xq, xs, Wq, Ws, group_off=None, *, ids=None, n_groups=None,
         if ids is not None or n_groups is not None:
             raise ValueError("group_off is required with ids or n_groups")
         Wq = Wq.unsqueeze(0)
-    D, dev = _linear_setup(xq, Wq, group_off, ids, n_groups, rows, torch.int8,
-                           (("xs", xs), ("Ws", Ws), ("y", y), ("counts", counts)),
-                           names=("xq", "Wq"))
+    D = _linear_dims(("xq", "Wq"), xq, Wq, group_off, ids, n_groups, rows, counts, torch.int8)
+    dev = xq.device
     _expect("xs", xs, D.T, torch.float32)
     _expect("Ws", Ws, D.E * D.out, torch.float32)
-    _expect("counts", counts, 4, torch.int32, optional=True)
-    y = _linear_out("y", y, D.M, D.out, out_dtype, dev)
-    D.out_dtype, D.flags = _out_code("y", y.dtype), OMNI_LINEAR_SILU if silu else 0
-    _on(dev, stream, "omni_quantized_linear",
-        (C.byref(D), _ptr(xq), _ptr(xs), _ptr(Wq), _ptr(Ws), _ptr(group_off), _ptr(ids),
-         _ptr(n_groups), _ptr(rows), _ptr(y), _ptr(counts)))
+    y, D.out_dtype = _linear_out("y", y, xq, D.M, D.out, out_dtype)
+    if silu:
+        D.flags = OMNI_LINEAR_SILU
+    _run("omni_quantized_linear", dev, stream, C.byref(D), _address("xq", xq, dev),
+         _address("xs", xs, dev), _address("Wq", Wq, dev), _address("Ws", Ws, dev),
+         _address("group_off", group_off, dev), _address("ids", ids, dev),
+         _address("n_groups", n_groups, dev), _address("rows", rows, dev),
+         _address("y", y, dev), _address("counts", counts, dev))
     return y
 
 

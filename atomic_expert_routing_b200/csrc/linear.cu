@@ -87,13 +87,18 @@ int omni_grouped_linear_backward(const omni_linear_dims* dims, const void* x, co
   a.dy = dy;
   a.accumulate = accumulate != 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (dx != nullptr && dims->M > 0) {
-    a.o = dx;
-    const int e = cuda_status(omni::launch_linear(Product::kGradX, a, s));
+  const bool form_dx = dx != nullptr && dims->M > 0;
+  const bool form_dW = dW != nullptr && (dims->M > 0 || !a.accumulate);
+  if (form_dx) {
+    LinearArgs b = a;
+    b.o = dx;
+    b.leads = form_dW;
+    const int e = cuda_status(omni::launch_linear(Product::kGradX, b, s));
     if (e != OMNI_OK) return e;
   }
-  if (dW != nullptr && (dims->M > 0 || !a.accumulate)) {
+  if (form_dW) {
     a.o = dW;
+    a.follows = form_dx;
     return cuda_status(omni::launch_linear(Product::kGradW, a, s));
   }
   return OMNI_OK;

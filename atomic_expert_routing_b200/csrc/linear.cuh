@@ -26,23 +26,28 @@ struct Groups {
 
 // Shared memory of build_groups beside the table: per-warp partial results
 // and the totals.
+constexpr int kGroupWarps = 8;
 struct GroupScratch {
-  int32_t off_max[32], id_max[32], tiles[32], used[32];
+  int32_t off_max[kGroupWarps], id_max[kGroupWarps], tiles[kGroupWarps], used[kGroupWarps];
   int32_t total_tiles, total_groups;
 };
 
-// Builds the table of the groups that have tiles, in order, with every
-// thread of the CTA (blockDim.x a multiple of 32, at most 1024); ends with a
-// CTA barrier.  tiles_of(rows): tiles of a group of that many rows, 0 to
-// leave it out.  A group counts only if its first offset is the largest
-// entry so far, its end is neither before that nor past M, and its id lies
-// in [0, E) above every earlier id: no two listed groups then share a row or
-// a matrix, whatever the arrays hold (G <= E, so without ids group g's is g).  status: where the bad-index bit goes
-// (one CTA passes it, the others nullptr).
+// Builds the table of the groups that have tiles, in order, with the CTA's
+// first kGroupWarps warps (the caller's barrier makes it visible).
+// tiles_of(rows): tiles of a group of that many rows, 0 to leave it out.  A
+// group counts only if its first offset is the largest entry so far, its end
+// is neither before that nor past M, and its id lies in [0, E) above every
+// earlier id: no two listed groups then share a row or a matrix, whatever
+// the arrays hold (G <= E, so without ids group g's is g).  status: where the
+// bad-index bit goes (one CTA passes it, the others nullptr).
+// The first round's entries are loaded beside the group count, and up to 32
+// groups need no exchange between warps: the table is the latency of one
+// load and some twenty shuffles, on the path of every call.
 template <class TilesOf>
 __device__ __forceinline__ void build_groups(const Groups& P, const TilesOf& tiles_of,
                                              GroupTab* tab, GroupScratch* sh, int32_t* status) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nwarps = blockDim.x >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int kThreads = 32 * kGroupWarps;
   if (P.off == nullptr) {
     if (tid == 0) {
       const int32_t rows = static_cast<int32_t>(P.M);
@@ -50,25 +55,33 @@ __device__ __forceinline__ void build_groups(const Groups& P, const TilesOf& til
       sh->total_tiles = tiles_of(rows);
       sh->total_groups = sh->total_tiles > 0 ? 1 : 0;
     }
-    __syncthreads();
     return;
   }
   int n = P.G;
   bool bad = false;
+  int32_t a = 0, b = 0, id = -1;
+  auto load = [&](int g) {  // G entries exist whatever the count says
+    const bool there = g < P.G;
+    a = there ? P.off[g] : 0;
+    b = there ? P.off[g + 1] : 0;
+    id = !there ? -1 : P.ids != nullptr ? P.ids[g] : g;
+  };
+  load(tid);
   if (P.n_groups != nullptr) {
     const int v = *P.n_groups;
     bad = v < 0 || v > n;
     n = v < 0 ? 0 : (v > n ? n : v);
   }
+  auto sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); };
   int32_t carry_off = 0, carry_id = -1, carry_tiles = 0, carry_used = 0;
-  for (int g0 = 0; g0 < n; g0 += blockDim.x) {
+  for (int g0 = 0; g0 < n; g0 += kThreads) {
     const int g = g0 + tid;
     const bool in = g < n;
-    const int32_t a = in ? P.off[g] : 0;
-    const int32_t b = in ? P.off[g + 1] : 0;
-    const int32_t id = in ? (P.ids != nullptr ? P.ids[g] : g) : -1;
+    if (g0 > 0) load(g);
+    const int warps = n - g0 > 32 * (kGroupWarps - 1) ? kGroupWarps : (n - g0 + 31) / 32;
+    if (warps == 1 && warp > 0) break;  // the last round is the first warp's
     // running maxima of the offsets (inclusive) and ids (exclusive)
-    int32_t mo = a, mi = id;
+    int32_t mo = in ? a : 0, mi = in ? id : -1;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int32_t po = __shfl_up_sync(0xffffffffu, mo, o);
@@ -78,25 +91,24 @@ __device__ __forceinline__ void build_groups(const Groups& P, const TilesOf& til
         mi = pi > mi ? pi : mi;
       }
     }
-    if (lane == 31) {
-      sh->off_max[warp] = mo;
-      sh->id_max[warp] = mi;
-    }
     int32_t mi_before = __shfl_up_sync(0xffffffffu, mi, 1);
     if (lane == 0) mi_before = -1;
-    __syncthreads();
-    int32_t all_off = carry_off, all_id = carry_id;
     int32_t before_off = carry_off, before_id = carry_id;
-    for (int w = 0; w < nwarps; ++w) {
-      if (w == warp) {
-        before_off = all_off;
-        before_id = all_id;
+    if (warps > 1) {
+      if (lane == 31) {
+        sh->off_max[warp] = mo;
+        sh->id_max[warp] = mi;
       }
-      all_off = sh->off_max[w] > all_off ? sh->off_max[w] : all_off;
-      all_id = sh->id_max[w] > all_id ? sh->id_max[w] : all_id;
+      sync();
+      for (int w = 0; w < warps; ++w) {
+        if (w == warp) {
+          before_off = carry_off;
+          before_id = carry_id;
+        }
+        carry_off = sh->off_max[w] > carry_off ? sh->off_max[w] : carry_off;
+        carry_id = sh->id_max[w] > carry_id ? sh->id_max[w] : carry_id;
+      }
     }
-    carry_off = all_off;
-    carry_id = all_id;
     mo = before_off > mo ? before_off : mo;
     mi_before = before_id > mi_before ? before_id : mi_before;
     const bool ok = in && a >= 0 && a == mo && b >= a && b <= P.M && id >= 0 && id < P.E &&
@@ -105,33 +117,36 @@ __device__ __forceinline__ void build_groups(const Groups& P, const TilesOf& til
     // places in the table; a bad group whose matrix is known is one without rows
     const int32_t rows = ok ? b - a : 0;
     const int32_t mine = ok || (in && P.ids == nullptr) ? tiles_of(rows) : 0;
-    int32_t st = mine, su = mine > 0 ? 1 : 0;
+    const unsigned with = __ballot_sync(0xffffffffu, mine > 0);
+    int32_t st = mine, before_t = 0, before_u = __popc(with & lanemask_lt());
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int32_t pt = __shfl_up_sync(0xffffffffu, st, o);
-      const int32_t pu = __shfl_up_sync(0xffffffffu, su, o);
-      if (lane >= o) {
-        st += pt;
-        su += pu;
-      }
+      if (lane >= o) st += pt;
     }
-    if (lane == 31) {
-      sh->tiles[warp] = st;
-      sh->used[warp] = su;
-    }
-    __syncthreads();
-    int32_t before_t = 0, before_u = 0, all_t = 0, all_u = 0;
-    for (int w = 0; w < nwarps; ++w) {
-      if (w == warp) {
-        before_t = all_t;
-        before_u = all_u;
+    int32_t all_t = 0, all_u = 0;
+    if (warps > 1) {
+      if (lane == 31) {
+        sh->tiles[warp] = st;
+        sh->used[warp] = __popc(with);
       }
-      all_t += sh->tiles[w];
-      all_u += sh->used[w];
+      sync();
+      int32_t u = 0;
+      for (int w = 0; w < warps; ++w) {
+        if (w == warp) {
+          before_t = all_t;
+          u = all_u;
+        }
+        all_t += sh->tiles[w];
+        all_u += sh->used[w];
+      }
+      before_u += u;
+    } else {
+      all_t = __shfl_sync(0xffffffffu, st, 31);
+      all_u = __popc(with);
     }
     if (mine > 0)
-      tab[carry_used + before_u + su - 1] =
-          GroupTab{carry_tiles + before_t + st - mine, a, rows, id};
+      tab[carry_used + before_u] = GroupTab{carry_tiles + before_t + st - mine, a, rows, id};
     carry_tiles += all_t;
     carry_used += all_u;
     // the next round writes the maxima before its first barrier and the sums
@@ -142,7 +157,6 @@ __device__ __forceinline__ void build_groups(const Groups& P, const TilesOf& til
     sh->total_groups = carry_used;
   }
   if (bad) raise_status(status, OMNI_DEV_BAD_INDEX);
-  __syncthreads();
 }
 
 // What the products of one launch read and write.
@@ -151,6 +165,7 @@ struct LinearArgs {
   int64_t T;
   int32_t in, out;
   int32_t out_f32, silu, accumulate;
+  int32_t leads, follows;  // dx and dW of one call, which may run side by side
   const int32_t* rows;  // nullable
   const void* x;        // [T x in]
   const void* W;        // [E x out x in]
