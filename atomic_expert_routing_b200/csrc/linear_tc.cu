@@ -20,11 +20,11 @@
 // the last block's in shared memory before its products.
 // CTAS = 2 pairs two CTAs on one 256-wide tile: each holds its half of A and
 // of B, and the pair's first CTA issues the MMAs.
-// Warps 0-7 drain the accumulators, warp 8 issues the TMA loads, warp 9 the
-// MMAs, warps 12-15 gather (10 and 11 fill their warpgroup); two TMEM accumulators alternate, so a tile is
+// Warps 0-7 drain the accumulators, warps 8 and 10 issue the TMA loads of A
+// and of B, warp 9 the MMAs, warps 12-15 gather (11 fills its warpgroup); two TMEM accumulators alternate, so a tile is
 // stored while the next is summed.
 //
-// PIECES: the tensor core's fp32 sums cut every addition towards zero, an
+// Pieces: the tensor core's fp32 sums cut every addition towards zero, an
 // error of about 1.1e-9 of the result per term of k.  bf16 results do not
 // show it; fp32 results are summed in pieces of 512 terms, which the draining
 // warps add up in registers, rounded to nearest.
@@ -40,16 +40,16 @@ constexpr int kBM = 128;            // i per CTA
 constexpr int kABytes = kBM * 128;  // a k-block's A tile: 128 bytes of k per row
 constexpr int kMaxStages = 12;
 constexpr int kEpiWarps = 8;
-constexpr int kLoadWarp = kEpiWarps, kMmaWarp = kEpiWarps + 1, kRowWarp = kEpiWarps + 4;
-constexpr int kRowWarps = 4, kRowThreads = 32 * kRowWarps;
+constexpr int kLoadWarp = kEpiWarps, kMmaWarp = kEpiWarps + 1, kLoadWarpB = kEpiWarps + 2;
+constexpr int kRowWarp = kEpiWarps + 4;
+constexpr int kRowWarps = 4;
 constexpr int kThreads = 32 * (kEpiWarps + 4 + kRowWarps);
 // Registers: 512 threads start with 128 each; the two draining warpgroups
 // (128 sums a thread) go to 184, the other two to 72: 2 * 184 + 2 * 72 = 4 * 128.
 constexpr int kLaunchRegs = 128, kEpiRegs = 184, kOtherRegs = 72;
 static_assert(2 * kEpiRegs + 2 * kOtherRegs == 4 * kLaunchRegs && kThreads == 512, "");
-// dW's tiles leave through shared memory: per half of the draining warps two
-// buffers of 16 columns of 128 fp32
-constexpr int kOutCols = 16, kOutBytes = kOutCols * kBM * 4;
+// Results leave through shared memory in chunks of 16 columns of 128
+constexpr int kOutCols = 16;
 constexpr int kPiece = 512;         // terms of k in a piece
 constexpr size_t kSmemLimit = 227 * 1024;
 
@@ -127,6 +127,14 @@ __device__ __forceinline__ void half_sync(int half) {
   else asm volatile("bar.sync 3, 128;" ::: "memory");
 }
 
+// shared memory -> a box of y or dx
+__device__ __forceinline__ void store_2d(const CUtensorMap* m, uint32_t src, int c0, int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(m),
+      "r"(src), "r"(c0), "r"(c1)
+      : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
 // shared memory -> a box of dW: written, or added
 __device__ __forceinline__ void store_3d(const CUtensorMap* m, uint32_t src, int c0, int c1,
                                          int c2, bool add) {
@@ -217,35 +225,43 @@ __device__ __forceinline__ void zero16(uint32_t dst) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst), "r"(0) : "memory");
 }
 
-// mbar_wait for barriers that the other CTA of a pair arrives on too
-__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
+// The bounded wait of this kernel: a try suspends its warp in hardware until
+// the phase ends or the hint (nanoseconds) runs out, so that the warps that
+// wait leave the issue slots to the warps that work; time-outs as mbar_wait.
+// CLUSTER: for barriers that the other CTA of a pair arrives on too.
+template <bool CLUSTER>
+__device__ __forceinline__ bool try_wait_for(uint32_t bar, uint32_t parity) {
+  constexpr uint32_t kHint = 20000;
   uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
+  if constexpr (CLUSTER)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(kHint)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(kHint)
+        : "memory");
   return ok != 0;
 }
-template <int CTAS>
-__device__ __forceinline__ bool wait_one(uint32_t bar, uint32_t parity, int32_t* status) {
-  if (CTAS == 1) return mbar_wait(bar, parity, status);
-  if (try_wait_cluster(bar, parity)) return true;
+template <bool CLUSTER>
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, int32_t* status) {
+  if (try_wait_for<CLUSTER>(bar, parity)) return true;
   const uint64_t t0 = global_ns();
-  for (uint32_t polls = 1; !try_wait_cluster(bar, parity); ++polls) {
+  for (uint32_t polls = 1; !try_wait_for<CLUSTER>(bar, parity); ++polls) {
     if (polls >= kWaitMaxPolls || global_ns() - t0 > kWaitLimitNs) {
       raise_status(status, OMNI_DEV_TIMEOUT);
       return false;
     }
   }
   return true;
-}
-// the same by a whole warp: the outcome is the same in every lane
-template <int CTAS>
-__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, int32_t* status) {
-  return __all_sync(0xffffffffu, wait_one<CTAS>(bar, parity, status));
 }
 
 // One lane of a converged warp.  tcgen05 and TMA instructions take their
@@ -278,6 +294,8 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
         "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
         "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait() {  // for the loads so far
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
@@ -285,10 +303,11 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
 
 struct Maps {
   CUtensorMap a, b;  // boxes of the two operands (a: W, or x for dW)
-  CUtensorMap out;   // dW
+  CUtensorMap whole;  // B in one box, where a tile has all its columns
+  CUtensorMap out;    // the result
 };
 
-template <Product P, int CTAS, int BN, bool PIECES>
+template <Product P, int CTAS, int BN, bool F32>
 struct Cfg {
   static constexpr bool kI8 = P == Product::kInt8;
   static constexpr bool kGradW = P == Product::kGradW, kGradX = P == Product::kGradX;
@@ -304,10 +323,18 @@ struct Cfg {
   static constexpr int kBBytes = kNb * 128;  // of a k-block
   static constexpr int kStageA = kSub * kABytes, kStageB = kSub * kBBytes;
   static constexpr int kStage = kStageA + kStageB;
-  static constexpr int kOut = kGradW ? 4 * kOutBytes : 0;  // dW's way out
+  static constexpr bool kPieces = F32 && !kI8;
+  static constexpr int kOutSize = F32 ? 4 : 2, kOutBytes = kOutCols * kBM * kOutSize;
+  // chunks each half of the draining warps may have on the way out
+  static constexpr int kOutBufs = BN >= 128 ? 4 : 1;
+  static constexpr int kOut = 2 * kOutBufs * kOutBytes;
   static constexpr int kCols = 2 * BN;            // TMEM columns
   static_assert(!kGradW || kNb % 64 == 0, "dW's B tile is made of 64-wide boxes");
 };
+
+// Whether dW's block of k with `left` rows to its group's end holds rows past
+// it that its last product (16 rows) would read.
+__device__ __forceinline__ bool has_tail(int left) { return left < 64 && (left & 15) != 0; }
 
 // One tile: columns j0 .. j0 + n - 1 of a group, i from i0.
 struct Tile {
@@ -335,13 +362,13 @@ struct TileWalk {
   }
 };
 
-template <Product P, int CTAS, int BN, bool PIECES>
+template <Product P, int CTAS, int BN, bool F32>
 __global__ void __launch_bounds__(kThreads, 1)
     k_linear_tc(const __grid_constant__ Maps maps, const __grid_constant__ LinearArgs a,
                 int stages) {
-  using C = Cfg<P, CTAS, BN, PIECES>;
+  using C = Cfg<P, CTAS, BN, F32>;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t bars[2 * kMaxStages + 5];
+  __shared__ uint64_t bars[3 * kMaxStages + 5];
   __shared__ uint32_t tmem_slot;
   __shared__ GroupScratch scratch;
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -349,26 +376,28 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t sA = smem_u32(smem), sB = sA + stages * C::kStageA;
   GroupTab* tab = reinterpret_cast<GroupTab*>(smem + stages * C::kStage + C::kOut);
   const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * kMaxStages;
-  const uint32_t tfull0 = empty0 + 8 * kMaxStages, tempty0 = tfull0 + 16, drain = tempty0 + 16;
+  const uint32_t tail0 = empty0 + 8 * kMaxStages;  // dW: a stage with rows to zero has landed
+  const uint32_t tfull0 = tail0 + 8 * kMaxStages, tempty0 = tfull0 + 16, drain = tempty0 + 16;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int rank = CTAS == 2 ? static_cast<int>(cluster_rank()) : 0;
   const int first = blockIdx.x / CTAS, step = gridDim.x / CTAS;
 
   const bool gathers = !C::kGradX && a.rows != nullptr;
-  // Where a half needs more than its TMA loads (gathered rows, rows to zero),
-  // each CTA of a pair waits for its own and the second tells the first;
-  // else the loads of both report to the first.
-  const bool halves = C::kGradW || gathers;
+  // With gathered rows each CTA of a pair waits for its own half and the
+  // second tells the first; else the loads of both report to the first.
+  const bool halves = gathers;
   if (threadIdx.x == 32 * kLoadWarp) {
     prefetch_map(&maps.a);
     prefetch_map(&maps.b);
-    // a stage is full after its loads' expect, its gathered rows, and in a
-    // pair's first CTA the second's word that its half is ready
-    const int arrivals =
-        1 + (gathers ? kRowThreads : 0) + (halves && CTAS == 2 && rank == 0 ? 1 : 0);
+    // A stage is full after its loads' two expects.  With gathered rows it is
+    // one expect, the threads of one row warp, and in a pair's first CTA the
+    // second's word that its half is ready.  Where dW has rows to zero, the
+    // row warps take the place of the expects.
+    const int arrivals = gathers ? 1 + 32 + (CTAS == 2 && rank == 0 ? 1 : 0) : 2;
     for (int s = 0; s < stages; ++s) {
       mbar_init(full0 + 8 * s, arrivals);
       mbar_init(empty0 + 8 * s, 1);
+      mbar_init(tail0 + 8 * s, gathers ? 1 : 2);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(tfull0 + 8 * b, 1);
@@ -409,22 +438,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp < kEpiWarps) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
     // ---- results: TMEM lane = i, column = j; a warp takes 32 lanes and every
-    // other chunk of 32 columns
+    // other chunk of 16 columns
     const int quarter = warp & 3, half = warp >> 2;
     const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
-    const uint32_t sOut = sB + stages * C::kStageB;
+    const uint32_t sOut = sB + stages * C::kStageB + half * C::kOutBufs * C::kOutBytes;
+    const bool issues = quarter == 0 && lane == 0;  // this half's stores
     uint32_t acc_no = 0, out_buf = 0;
     bool ok = true;
     for (int t = first; t < tiles && ok; t += step) {
       const Tile tl = walk.at(t);
-      const int i = tl.i0 + rank * kBM + 32 * quarter + lane;
-      const int pieces = PIECES ? (tl.K + kPiece - 1) / kPiece : 1;
+      const int ic = tl.i0 + rank * kBM, i = ic + 32 * quarter + lane;
       float ws = 0.0f;
       if (C::kI8 && i < I) ws = a.Ws[static_cast<int64_t>(tl.id) * a.out + i];
 
       auto wait_full = [&]() -> bool {
-        const bool got =
-            __all_sync(0xffffffffu, mbar_wait(tfull0 + 8 * (acc_no & 1), (acc_no >> 1) & 1, a.status));
+        const bool got = __all_sync(
+            0xffffffffu, wait_for<false>(tfull0 + 8 * (acc_no & 1), (acc_no >> 1) & 1, a.status));
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         return got;
       };
@@ -438,177 +467,186 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ++acc_no;
       };
-      // dW: 16 columns from c to shared memory, and from there by TMA, while the
-      // next 16 go to the other buffer
-      auto leave = [&](int c, const float* v) {
-        const bool issues = quarter == 0 && lane == 0;
-        const uint32_t buf = sOut + (2 * half + out_buf) * kOutBytes;
-        if (issues) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-        half_sync(half);
+      // columns c .. c + 15 of this lane's i leave.  A whole chunk goes through
+      // shared memory and from there by TMA, which writes full lines and clips
+      // i (the warps' own stores, 64 or 128 bytes each, cost about 10 cycles
+      // apiece and bounded short sums); columns cut by a group's end are
+      // stored one by one.  dW's columns end with the matrix, where TMA clips.
+      auto leave = [&](int c, const float* z) {
+        const int n = tl.n - c;
+        if (ic >= I) return;
+        if (C::kGradW || n >= kOutCols) {
+          const uint32_t buf = sOut + out_buf * C::kOutBytes;
+          if (issues)
+            asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(C::kOutBufs - 1) : "memory");
+          half_sync(half);
 #pragma unroll
-        for (int q = 0; q < kOutCols; ++q)
-          asm volatile("st.shared.f32 [%0], %1;" ::"r"(buf + (q * kBM + 32 * quarter + lane) * 4),
-                       "f"(v[q])
-                       : "memory");
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        half_sync(half);
-        if (issues)
-          store_3d(&maps.out, buf, tl.i0 + rank * kBM, tl.j0 + c, tl.id, a.accumulate != 0);
-        out_buf ^= 1;
-      };
-      // columns c .. c + 31 of this lane's i
-      auto store = [&](int c, const float* v) {
-        const int n = tl.n - c;  // columns that exist
-        {
-          const int64_t at = static_cast<int64_t>(tl.row0 + tl.j0 + c) * I;
-          float z[32];
-          float xs = 0.0f;
-          if (C::kI8 && lane < n) {
-            const int r = tl.row0 + tl.j0 + c + lane;
-            int xr = r;
-            if (a.rows != nullptr) {
-              xr = a.rows[r];
-              if (xr < 0 || xr >= a.T) xr = 0;
-            }
-            xs = a.xs[xr];
+          for (int q = 0; q < kOutCols; ++q) {
+            const uint32_t to = buf + (q * kBM + 32 * quarter + lane) * C::kOutSize;
+            if constexpr (F32)
+              asm volatile("st.shared.f32 [%0], %1;" ::"r"(to), "f"(z[q]) : "memory");
+            else
+              asm volatile("st.shared.b16 [%0], %1;" ::"r"(to),
+                           "h"(__bfloat16_as_ushort(__float2bfloat16_rn(z[q])))
+                           : "memory");
           }
-#pragma unroll
-          for (int q = 0; q < 32; ++q) {
-            z[q] = v[q];
-            if constexpr (C::kI8)
-              z[q] = static_cast<float>(__float_as_int(v[q])) *
-                     __shfl_sync(0xffffffffu, xs, q) * ws;
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          half_sync(half);
+          if (issues) {
+            if constexpr (C::kGradW)
+              store_3d(&maps.out, buf, ic, tl.j0 + c, tl.id, a.accumulate != 0);
+            else
+              store_2d(&maps.out, buf, ic, tl.row0 + tl.j0 + c);
           }
-          if (a.silu) {
-            if (a.out_f32) {
+          if (++out_buf == C::kOutBufs) out_buf = 0;
+        } else if (i < I) {
+          const int64_t at = static_cast<int64_t>(tl.row0 + tl.j0 + c) * I + i;
 #pragma unroll
-              for (int q = 0; q < 32; ++q) z[q] = silu(z[q]);
-            } else {
-#pragma unroll
-              for (int q = 0; q < 32; ++q) z[q] = silu_fast(z[q]);
+          for (int q = 0; q < kOutCols; ++q)
+            if (q < n) {
+              if constexpr (F32)
+                static_cast<float*>(a.o)[at + static_cast<int64_t>(q) * I] = z[q];
+              else
+                static_cast<__nv_bfloat16*>(a.o)[at + static_cast<int64_t>(q) * I] =
+                    __float2bfloat16_rn(z[q]);
             }
-          }
-          if (a.out_f32) {
-            float* o = static_cast<float*>(a.o) + at + i;
-            if (i < I) {
-#pragma unroll
-              for (int q = 0; q < 32; ++q)
-                if (q < n) o[static_cast<int64_t>(q) * I] = z[q];
-            }
-          } else {
-            // two lanes trade so that each stores two neighbours of one column
-            const bool odd = lane & 1;
-            __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.o) + at + (i & ~1);
-#pragma unroll
-            for (int q = 0; q < 32; q += 2) {
-              const float got = __shfl_xor_sync(0xffffffffu, odd ? z[q] : z[q + 1], 1);
-              const __nv_bfloat162 w =
-                  odd ? __floats2bfloat162_rn(got, z[q + 1]) : __floats2bfloat162_rn(z[q], got);
-              if (i < I && q + (odd ? 1 : 0) < n)
-                *reinterpret_cast<__nv_bfloat162*>(o + static_cast<int64_t>(q + (odd ? 1 : 0)) * I) = w;
-            }
-          }
         }
       };
-
-      if constexpr (PIECES) {
-        constexpr int kAcc = BN > 32 ? BN / 2 : 32;  // columns of this warp
-        float sum[kAcc];
+      // the scale of column c + lane (lanes 0 .. 15) or c + 16 + lane (16 .. 31)
+      auto token_scale = [&](int c) -> float {
+        const int j = c + lane + (lane < 16 ? 0 : 16);
+        if (!C::kI8 || j >= tl.n) return 0.0f;
+        const int r = tl.row0 + tl.j0 + j;
+        if (a.rows == nullptr) return a.xs[r];
+        const int v = a.rows[r];
+        return a.xs[v >= 0 && v < a.T ? v : 0];
+      };
+      auto finish = [&](int c, float* z, float xs, int from) {
+        if constexpr (C::kI8) {
 #pragma unroll
-        for (int q = 0; q < kAcc; ++q) sum[q] = 0.0f;
-        for (int p = 0; p < pieces && ok; ++p) {
+          for (int q = 0; q < kOutCols; ++q)
+            z[q] = static_cast<float>(__float_as_int(z[q])) *
+                   __shfl_sync(0xffffffffu, xs, from + q) * ws;
+        }
+        if (!C::kGradW && a.silu) {
+#pragma unroll
+          for (int q = 0; q < kOutCols; ++q) z[q] = F32 ? silu(z[q]) : silu_fast(z[q]);
+        }
+        leave(c, z);
+      };
+
+      if constexpr (C::kPieces) {
+        constexpr int kMine = BN / 32;  // chunks of this warp
+        float sum[kMine][kOutCols];
+#pragma unroll
+        for (int u = 0; u < kMine; ++u)
+#pragma unroll
+          for (int q = 0; q < kOutCols; ++q) sum[u][q] = 0.0f;
+        for (int k0 = 0; k0 < tl.K; k0 += kPiece) {
           ok = wait_full();
           if (!ok) break;
 #pragma unroll
-          for (int u = 0; u < kAcc / 32; ++u) {
-            const int c = (2 * u + half) * 32;
+          for (int u = 0; u < kMine; ++u) {
+            const int c = (2 * u + half) * kOutCols;
             if (c < tl.n) {
+              uint32_t v[kOutCols];
+              tmem_ld16(tmem + lanes + (acc_no & 1) * BN + c, v);
+              tmem_wait();
 #pragma unroll
-              for (int w = 0; w < 32; w += 16) {
-                uint32_t v[16];
-                tmem_ld16(tmem + lanes + (acc_no & 1) * BN + c + w, v);
-#pragma unroll
-                for (int q = 0; q < 16; ++q) sum[u * 32 + w + q] += __uint_as_float(v[q]);
-              }
+              for (int q = 0; q < kOutCols; ++q) sum[u][q] += __uint_as_float(v[q]);
             }
           }
           drained();
         }
         if (!ok) break;
 #pragma unroll
-        for (int u = 0; u < kAcc / 32; ++u) {
-          const int c = (2 * u + half) * 32;
-          if constexpr (C::kGradW) {
-#pragma unroll
-            for (int w = 0; w < 32; w += kOutCols)
-              if (c + w < tl.n && tl.i0 + rank * kBM < I) leave(c + w, sum + u * 32 + w);
-          } else {
-            if (c < tl.n) store(c, sum + u * 32);
-          }
+        for (int u = 0; u < kMine; ++u) {
+          const int c = (2 * u + half) * kOutCols;
+          if (c < tl.n) finish(c, sum[u], 0.0f, 0);
         }
       } else {
+        // two chunks at a time
+        float xs = token_scale(half * kOutCols);
         ok = wait_full();
         if (!ok) break;
-        for (int c = half * 32; c < tl.n; c += 64) {
-          uint32_t v[32];
-          tmem_ld32(tmem + lanes + (acc_no & 1) * BN + c, v);
-          store(c, reinterpret_cast<const float*>(v));
+        const uint32_t acc = tmem + lanes + (acc_no & 1) * BN;
+        for (int c = half * kOutCols; c < tl.n; c += 4 * kOutCols) {
+          uint32_t v[2][kOutCols];
+          tmem_ld16(acc + c, v[0]);
+          const bool both = BN > 2 * kOutCols && c + 2 * kOutCols < tl.n;
+          if (both) tmem_ld16(acc + c + 2 * kOutCols, v[1]);
+          tmem_wait();
+          const float scale = xs;
+          if (c + 4 * kOutCols < tl.n) xs = token_scale(c + 4 * kOutCols);
+          else drained();
+          finish(c, reinterpret_cast<float*>(v[0]), scale, 0);
+          if (both) finish(c + 2 * kOutCols, reinterpret_cast<float*>(v[1]), scale, 16);
         }
-        drained();
+        if (half * kOutCols >= tl.n) drained();
       }
     }
-    if (C::kGradW)  // this thread's stores are done
-      asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // this thread's stores are done
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp == kLoadWarp) {
-      // ---- TMA loads
-      if (elect_one()) {
+    if (warp == kLoadWarp || warp == kLoadWarpB) {
+      // ---- TMA loads: one warp for each operand that is not gathered (a load
+      // costs its thread about 70 cycles, a stage's products 512)
+      const bool loads_a = warp == kLoadWarp;
+      if (!(gathers && loads_a == C::kGradW) && elect_one()) {
         int s = 0;
         uint32_t ph = 0, issued = 0;
+        uint32_t tails = 0;  // dW: parity of each stage's uses of its tail barrier
         bool ok = true;
         for (int t = first; t < tiles && ok; t += step) {
           const Tile tl = walk.at(t);
           const int nb = n_mma(tl) / CTAS;  // j of this CTA: j0 + rank * nb ..
           const int i0 = tl.i0 + rank * kBM, j0 = tl.j0 + rank * nb;
           const int boxes = (nb + C::kBox - 1) / C::kBox;
-          const uint32_t bytes = (C::kGradW && gathers ? 0 : kABytes) +
-                                 (!C::kGradW && gathers ? 0 : boxes * C::kBox * 128);
+          const uint32_t bytes = loads_a ? kABytes : boxes * C::kBox * 128;
           for (int k0 = 0; k0 < tl.K; k0 += C::kStageK) {
             const uint32_t own = full0 + 8 * s;
-            const uint32_t bar = CTAS == 2 && !halves ? leader_addr(own) : own;
-            if (!mbar_wait(empty0 + 8 * s, ph ^ 1, a.status)) {
+            if (!wait_for<false>(empty0 + 8 * s, ph ^ 1, a.status)) {
               ok = false;
               break;
             }
             const int subs = C::kSub == 1 || tl.K - k0 <= C::kBlockK ? 1 : 2;
-            if (halves)
+            uint32_t bar = CTAS == 2 && !halves ? leader_addr(own) : own;
+            if (C::kGradW && has_tail(tl.K - k0)) {
+              // the row warps see these loads first, zero rows, and fill the stage
+              bar = tail0 + 8 * s;
+              mbar_expect_tx(bar, bytes);
+              tails ^= 1u << s;
+              if (gathers) mbar_arrive(own);
+            } else if (halves) {
               mbar_expect_tx(own, subs * bytes);
-            else if (rank == 0)
+            } else if (rank == 0) {
               mbar_expect_tx(own, CTAS * subs * bytes);
+            }
 #pragma unroll
             for (int u = 0; u < C::kSub; ++u) {
               if (u >= subs) break;
               const uint32_t da = sA + s * C::kStageA + u * kABytes;
               const uint32_t db = sB + s * C::kStageB + u * C::kBBytes;
               const int k = k0 + u * C::kBlockK;
-              if constexpr (C::kGradW) {
-                if (!gathers)
+              if (loads_a) {
+                if constexpr (C::kGradW) {
                   for (int h = 0; h < 2; ++h)
-                    load_2d<1>(da + h * 8192, &maps.a, bar, i0 + 64 * h, tl.row0 + k);
-                for (int h = 0; h < boxes; ++h)
-                  load_2d<1>(db + h * 8192, &maps.b, bar, j0 + 64 * h, tl.row0 + k);
-              } else {
-                if constexpr (C::kGradX) {
+                    load_2d<CTAS>(da + h * 8192, &maps.a, bar, i0 + 64 * h, tl.row0 + k);
+                } else if constexpr (C::kGradX) {
                   for (int h = 0; h < 2; ++h)
                     load_3d<CTAS>(da + h * 8192, &maps.a, bar, i0 + 64 * h, k, tl.id);
                 } else {
                   load_3d<CTAS>(da, &maps.a, bar, k, i0, tl.id);
                 }
-                if (!gathers)
-                  for (int q = 0; q < boxes; ++q)
-                    load_2d<CTAS>(db + q * C::kBox * 128, &maps.b, bar, k,
-                                  tl.row0 + j0 + q * C::kBox);
+              } else if constexpr (C::kGradW) {
+                for (int h = 0; h < boxes; ++h)
+                  load_2d<CTAS>(db + h * 8192, &maps.b, bar, j0 + 64 * h, tl.row0 + k);
+              } else if (nb == C::kNb) {
+                load_2d<CTAS>(db, &maps.whole, bar, k, tl.row0 + j0);
+              } else {
+                for (int q = 0; q < boxes; ++q)
+                  load_2d<CTAS>(db + q * C::kBox * 128, &maps.b, bar, k,
+                                tl.row0 + j0 + q * C::kBox);
               }
             }
             ++issued;
@@ -621,21 +659,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) {
           // a wait timed out: the loads in flight land (each wait bounded again)
           // before the CTA exits
+          if (C::kGradW)
+            for (int q = 0; q < stages; ++q)
+              wait_for<false>(tail0 + 8 * q, ((tails >> q) & 1) ^ 1, a.status);
           if (rank == 0 || halves)
             for (uint32_t k = issued > static_cast<uint32_t>(stages) ? issued - stages : 0u;
                  k < issued; ++k)
-              mbar_wait(full0 + 8 * (k % stages), (k / stages) & 1, a.status);
+              wait_for<false>(full0 + 8 * (k % stages), (k / stages) & 1, a.status);
         }
       }
     } else if (warp == kMmaWarp) {
-      // ---- products: issued by one lane of the pair's first CTA.  dW keeps the
-      // whole warp in step, to zero rows.
-      constexpr bool kWarp = C::kGradW;
-      if ((rank == 0 || halves) && (kWarp || elect_one())) {
-        auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
-          if (kWarp) return wait_warp<CTAS>(bar, parity, a.status);
-          return wait_one<CTAS>(bar, parity, a.status);
-        };
+      // ---- products: issued by one lane of the pair's first CTA
+      if ((rank == 0 || halves) && elect_one()) {
         int s = 0;
         uint32_t ph = 0, acc_no = 0;
         bool ok = true;
@@ -649,39 +684,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t acc = 0;
           for (int k0 = 0; k0 < tl.K; k0 += C::kStageK) {
             const int left = tl.K - k0;
-            const bool starts = k0 % (PIECES ? kPiece : 1 << 30) == 0;
+            const bool starts = k0 % (C::kPieces ? kPiece : 1 << 30) == 0;
             const bool ends =
-                left <= C::kStageK || (PIECES && (k0 + C::kStageK) % kPiece == 0);
+                left <= C::kStageK || (C::kPieces && (k0 + C::kStageK) % kPiece == 0);
             if (starts && rank == 0) {
               const uint32_t b = acc_no & 1;
-              ok = wait(tempty0 + 8 * b, ((acc_no >> 1) & 1) ^ 1);
+              ok = wait_for<CTAS == 2>(tempty0 + 8 * b, ((acc_no >> 1) & 1) ^ 1, a.status);
               if (!ok) break;
               asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
               acc = tmem + b * BN;
             }
             const uint32_t da = sA + s * C::kStageA, db = sB + s * C::kStageB;
-            ok = wait(full0 + 8 * s, ph);
+            ok = wait_for<CTAS == 2>(full0 + 8 * s, ph, a.status);
             if (!ok) break;
-            if constexpr (C::kGradW) {
-              // rows past the group's end, up to the last product's 16: zeros (of
-              // both operands: what is there may be infinite)
-              if (left < C::kBlockK && (left & 15) != 0) {
-                const int rows = 16 - (left & 15), nb = n_mma(tl) / CTAS;
-                for (int g = lane; g < rows * 8; g += 32) {
-                  const uint32_t at = (left + (g >> 3)) * 128 + (g & 7) * 16;
-                  if (!gathers)
-                    for (int h = 0; h < 2; ++h) zero16(da + h * 8192 + at);
-                  for (int h = 0; h < (nb + 63) / 64; ++h) zero16(db + h * 8192 + at);
-                }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-              }
-            }
             // rows copied by threads, before the tensor core reads them
             if (gathers) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            if (kWarp) __syncwarp();
             if (rank != 0) {  // this half is ready
-              if (!kWarp || lane == 0) arrive_cluster(leader_addr(full0 + 8 * s));
-            } else if (!kWarp || elect_one()) {
+              arrive_cluster(leader_addr(full0 + 8 * s));
+            } else {
               asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
               const int steps = left >= C::kStageK ? C::kStageK / C::kMmaK
                                                    : (left + C::kMmaK - 1) / C::kMmaK;
@@ -699,7 +719,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               commit<CTAS>(empty0 + 8 * s);
               if (ends) commit<CTAS>(tfull0 + 8 * (acc_no & 1));
             }
-            if (kWarp) __syncwarp();
             if (ends) ++acc_no;
             if (++s == stages) {
               s = 0;
@@ -709,124 +728,168 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok) {
           // the MMAs in flight end (bounded) before TMEM is freed
-          if (rank == 0 && (!kWarp || elect_one())) {
+          if (rank == 0) {
             commit<CTAS>(drain);
-            mbar_wait(drain, 0, a.status);
+            wait_for<false>(drain, 0, a.status);
           }
         }
       }
     } else if (warp >= kRowWarp) {
-      // ---- x's rows by token: 16 bytes a copy, eight copies to a row's 128 bytes
-      if (gathers) {
-        constexpr int kRows = C::kGradW ? 64 : C::kNb;         // of a stage
-        constexpr int kMine = (kRows + kRowThreads / 8 - 1) / (kRowThreads / 8);
-        const int tid = threadIdx.x - 32 * kRowWarp;
-        const int r0 = tid >> 3, piece = tid & 7;
-        const uint32_t place = static_cast<uint32_t>((piece ^ (r0 & 7)) * 16);  // swizzled
-        const int64_t pitch = static_cast<int64_t>(a.in) * (C::kI8 ? 1 : 2);
-        const char* x = static_cast<const char*>(a.x);
-        auto checked = [&](int v) -> int {  // a row number as the caller gave it
-          if (v >= 0 && v < a.T) return v;
-          raise_status(a.status, OMNI_DEV_BAD_INDEX);
-          return 0;
-        };
-        int s = 0;
-        uint32_t ph = 0;
-        bool ok = true;
+      // ---- x's rows by token, and dW's rows past a group's end.  The warps take
+      // the stages in turn, one each: a stage costs a warp some 650 cycles of
+      // waits, arrival and bookkeeping beside its copies (16 bytes a thread,
+      // eight threads to a row's 128 bytes, four rows at a time).
+      const int mine = warp - kRowWarp;
+      const int sub = lane >> 3, piece = lane & 7;
+      // where the copy of row 4 q + sub goes: even and odd q (swizzled)
+      const uint32_t even = static_cast<uint32_t>(sub * 128 + ((piece ^ sub) * 16));
+      const uint32_t odd = even ^ 64u;
+      const int64_t pitch = static_cast<int64_t>(a.in) * (C::kI8 ? 1 : 2);
+      const char* x = static_cast<const char*>(a.x);
+      auto checked = [&](int v) -> int {  // a row number as the caller gave it
+        if (v >= 0 && v < a.T) return v;
+        raise_status(a.status, OMNI_DEV_BAD_INDEX);
+        return 0;
+      };
+      auto wait_empty = [&](uint32_t no, int* s) -> bool {  // stage number no
+        *s = static_cast<int>(no % stages);
+        const uint32_t ph = (no / stages) & 1;
+        return __all_sync(0xffffffffu, wait_for<false>(empty0 + 8 * *s, ph ^ 1, a.status));
+      };
+      uint32_t no = 0;  // of the tile's first stage
+      bool ok = true;
+      if constexpr (C::kGradW) {
+        uint32_t tails = 0;
         for (int t = first; t < tiles && ok; t += step) {
           const Tile tl = walk.at(t);
-          const int nb = n_mma(tl) / CTAS;
-          const int i0 = tl.i0 + rank * kBM;
-          const int mine = tl.n - rank * nb;  // dW: unused; else rows of this CTA
-          const int row0 = C::kGradW ? tl.row0 : tl.row0 + tl.j0 + rank * nb;
-          // dW takes other rows every block: each lane reads two of the block's
-          // 64 row numbers, three blocks ahead
-          int2 ahead[3];
-          auto fetch = [&](int kb) -> int2 {
-            const int r = kb * 64 + lane;
-            return make_int2(r < tl.K ? a.rows[row0 + r] : -1,
-                             r + 32 < tl.K ? a.rows[row0 + r + 32] : -1);
-          };
-          const char* src[kMine];
-          if constexpr (C::kGradW) {
-#pragma unroll
-            for (int q = 0; q < 3; ++q) ahead[q] = fetch(q);
-          } else {
-#pragma unroll
-            for (int q = 0; q < kMine; ++q) {
-              const int r = r0 + q * (kRowThreads / 8);
-              // (past the group's end any row will do: its column is not stored)
-              const int row = r < mine && r < kRows ? checked(a.rows[row0 + r]) : 0;
-              src[q] = x + row * pitch + 16 * piece;
+          const int blocks = (tl.K + 63) / 64, last = tl.K - 64 * (blocks - 1);
+          const bool tail = blocks > 0 && has_tail(last);
+          const int tail_s = static_cast<int>((no + blocks - 1) % stages);
+          // zeroes the rows past the group's end up to the last product's 16, of
+          // both operands: what is there may be infinite
+          auto zero_tail = [&]() {
+            ok = __all_sync(0xffffffffu, wait_for<false>(tail0 + 8 * tail_s,
+                                                         (tails >> tail_s) & 1, a.status));
+            if (!ok) return;
+            const uint32_t da = sA + tail_s * C::kStageA, db = sB + tail_s * C::kStageB;
+            const int chunks = (n_mma(tl) / CTAS + 63) / 64;
+            for (int g = lane; g < (16 - (last & 15)) * 8; g += 32) {
+              const uint32_t at = (last + (g >> 3)) * 128 + (g & 7) * 16;
+              if (!gathers)
+                for (int h = 0; h < 2; ++h) zero16(da + h * 8192 + at);
+              for (int h = 0; h < chunks; ++h) zero16(db + h * 8192 + at);
             }
-          }
-          for (int k0 = 0; k0 < tl.K; k0 += C::kStageK) {
-            ok = __all_sync(0xffffffffu, mbar_wait(empty0 + 8 * s, ph ^ 1, a.status));
-            if (!ok) break;
-            if constexpr (C::kGradW) {
-              const int left = tl.K - k0;
-              const int2 v = make_int2(lane < left ? checked(ahead[0].x) : -1,
-                                       lane + 32 < left ? checked(ahead[0].y) : -1);
-              ahead[0] = ahead[1];
-              ahead[1] = ahead[2];
-              ahead[2] = fetch(k0 / 64 + 3);
-              const uint32_t da = sA + s * C::kStageA + r0 * 128 + place;
-              const int c = i0 + 8 * piece;
-              const char* xc = x + static_cast<int64_t>(c) * 2;
-              const bool whole = left >= 64 && i0 + kBM <= a.in;
-              auto row_of = [&](int q) -> int {
-                return __shfl_sync(0xffffffffu, q < kMine / 2 ? v.x : v.y,
-                                   (r0 + q * (kRowThreads / 8)) & 31);
-              };
-              if (whole) {
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          };
+          if (gathers) {
+            const int c = tl.i0 + rank * kBM + 8 * piece;  // column of x
+            const char* xc = x + static_cast<int64_t>(c) * 2;
+            const bool wide = tl.i0 + rank * kBM + kBM <= a.in;
+            auto fetch = [&](int kb) -> int2 {  // a block's 64 row numbers
+              const int r = 64 * kb + lane;
+              return make_int2(r < tl.K ? a.rows[tl.row0 + r] : 0,
+                               r + 32 < tl.K ? a.rows[tl.row0 + r + 32] : 0);
+            };
+            int kb = static_cast<int>((mine - no) & (kRowWarps - 1));
+            int2 ahead = fetch(kb);
+            for (; kb < blocks; kb += kRowWarps) {
+              const int left = tl.K - 64 * kb;
+              const int lo = lane < left ? checked(ahead.x) : -1;
+              const int hi = lane + 32 < left ? checked(ahead.y) : -1;
+              ahead = fetch(kb + kRowWarps);
+              int s;
+              ok = wait_empty(no + kb, &s);
+              if (!ok) break;
+              const uint32_t to = sA + s * C::kStageA;
+              if (wide && left >= 64) {
 #pragma unroll
-                for (int q = 0; q < kMine; ++q) {
-                  const char* p = xc + row_of(q) * pitch;
-                  copy16(da + q * (kRowThreads / 8) * 128, p);
-                  copy16(da + q * (kRowThreads / 8) * 128 + 8192, p + 128);
+                for (int q = 0; q < 16; ++q) {
+                  const int row = __shfl_sync(0xffffffffu, q < 8 ? lo : hi, (4 * q + sub) & 31);
+                  const char* p = xc + row * pitch;
+                  copy16(to + q * 512 + (q & 1 ? odd : even), p);
+                  copy16(to + q * 512 + (q & 1 ? odd : even) + 8192, p + 128);
                 }
               } else {
 #pragma unroll
-                for (int q = 0; q < kMine; ++q) {
-                  const int row = row_of(q);
+                for (int q = 0; q < 16; ++q) {
+                  const int row = __shfl_sync(0xffffffffu, q < 8 ? lo : hi, (4 * q + sub) & 31);
 #pragma unroll
                   for (int h = 0; h < 2; ++h) {
                     const bool in = row >= 0 && c + 64 * h < a.in;
-                    copy16_or_zero(da + q * (kRowThreads / 8) * 128 + h * 8192,
+                    copy16_or_zero(to + q * 512 + (q & 1 ? odd : even) + h * 8192,
                                    in ? xc + row * pitch + 128 * h : x, in);
                   }
                 }
               }
-            } else {
-              const uint32_t db = sB + s * C::kStageB + r0 * 128 + place;
+              if (tail && kb == blocks - 1) {
+                zero_tail();
+                if (!ok) break;
+              }
+              copies_arrive(full0 + 8 * s);
+            }
+          } else if (tail && ((no + blocks - 1) & (kRowWarps - 1)) == mine) {
+            zero_tail();
+            __syncwarp();
+            if (ok && lane == 0) {  // in place of the loads' two expects
+              if (CTAS == 2) {
+                arrive_cluster(leader_addr(full0 + 8 * tail_s));
+              } else {
+                mbar_arrive(full0 + 8 * tail_s);
+                mbar_arrive(full0 + 8 * tail_s);
+              }
+            }
+          }
+          if (tail) tails ^= 1u << tail_s;
+          no += blocks;
+        }
+      } else if (gathers) {
+        for (int t = first; t < tiles && ok; t += step) {
+          const Tile tl = walk.at(t);
+          const int nb = n_mma(tl) / CTAS;
+          const int there = tl.n - rank * nb, row0 = tl.row0 + tl.j0 + rank * nb;
+          const int blocks = (tl.K + C::kStageK - 1) / C::kStageK;
+          // the tile's row numbers, 32 to a register of the warp (past the
+          // group's end any row will do: its column is not stored)
+          int at[(C::kNb + 31) / 32];
 #pragma unroll
-              for (int u = 0; u < C::kSub; ++u) {
-                const int k = k0 + u * C::kBlockK;
-                if (k >= tl.K) break;
-                const int64_t c = static_cast<int64_t>(k) * (C::kI8 ? 1 : 2);  // bytes
-                const bool whole = k + C::kBlockK <= tl.K, in = c + 16 * piece < pitch;
-                const uint32_t to = db + u * C::kBBytes;
-                if (whole) {
+          for (int h = 0; h < (C::kNb + 31) / 32; ++h)
+            at[h] = 32 * h + lane < there ? checked(a.rows[row0 + 32 * h + lane]) : 0;
+          for (int kb = static_cast<int>((mine - no) & (kRowWarps - 1)); kb < blocks;
+               kb += kRowWarps) {
+            int s;
+            ok = wait_empty(no + kb, &s);
+            if (!ok) break;
 #pragma unroll
-                  for (int q = 0; q < kMine; ++q)
-                    if (q * (kRowThreads / 8) < nb) copy16(to + q * (kRowThreads / 8) * 128, src[q] + c);
-                } else {
+            for (int u = 0; u < C::kSub; ++u) {
+              const int k = kb * C::kStageK + u * C::kBlockK;
+              if (k >= tl.K) break;
+              const uint32_t to = sB + s * C::kStageB + u * C::kBBytes;
+              const int64_t c = static_cast<int64_t>(k) * (C::kI8 ? 1 : 2) + 16 * piece;  // bytes
+              const char* xc = x + c;
+              if (k + C::kBlockK <= tl.K) {
 #pragma unroll
-                  for (int q = 0; q < kMine; ++q)
-                    if (q * (kRowThreads / 8) < nb)
-                      copy16_or_zero(to + q * (kRowThreads / 8) * 128, in ? src[q] + c : x, in);
-                }
+                for (int q = 0; q < C::kNb / 4; ++q)
+                  if (4 * q < nb) {
+                    const int row = __shfl_sync(0xffffffffu, at[q / 8], (4 * q + sub) & 31);
+                    copy16(to + q * 512 + (q & 1 ? odd : even), xc + row * pitch);
+                  }
+              } else {
+                const bool in = c < pitch;
+#pragma unroll
+                for (int q = 0; q < C::kNb / 4; ++q)
+                  if (4 * q < nb) {
+                    const int row = __shfl_sync(0xffffffffu, at[q / 8], (4 * q + sub) & 31);
+                    copy16_or_zero(to + q * 512 + (q & 1 ? odd : even),
+                                   in ? xc + row * pitch : x, in);
+                  }
               }
             }
             copies_arrive(full0 + 8 * s);
-            if (++s == stages) {
-              s = 0;
-              ph ^= 1;
-            }
           }
+          no += blocks;
         }
-        asm volatile("cp.async.wait_all;" ::: "memory");
       }
+      asm volatile("cp.async.wait_all;" ::: "memory");
     }
   }
   __syncwarp();
@@ -864,16 +927,16 @@ bool make_map_nd(CUtensorMap* m, const void* base, CUtensorMapDataType type, int
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <Product P, int CTAS, int BN, bool PIECES>
+template <Product P, int CTAS, int BN, bool F32>
 cudaError_t launch(const LinearArgs& a, cudaStream_t s) {
-  using C = Cfg<P, CTAS, BN, PIECES>;
+  using C = Cfg<P, CTAS, BN, F32>;
   Maps m{};
   const int64_t W[3] = {a.in, a.out, a.g.E}, X[2] = {a.in, a.T}, Y[2] = {a.out, a.g.M};
   const int kb = C::kBlockK, esize = C::kI8 ? 1 : 2;
   const CUtensorMapDataType type =
       C::kI8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const int box_w[3] = {kb, C::kMnA ? 64 : kBM, 1}, box_r[2] = {kb, C::kBox};
-  const int box_64[2] = {64, 64};
+  const int box_b[2] = {kb, C::kNb}, box_64[2] = {64, 64};
   bool ok = true;
   if (a.g.M > 0) {
     if (C::kGradW) {
@@ -881,24 +944,26 @@ cudaError_t launch(const LinearArgs& a, cudaStream_t s) {
            make_map_nd(&m.b, a.dy, type, esize, 2, Y, box_64);
     } else {
       ok = make_map_nd(&m.a, a.W, type, esize, 3, W, box_w) &&
-           make_map_nd(&m.b, C::kGradX ? a.dy : a.x, type, esize, 2, C::kGradX ? Y : X, box_r);
+           make_map_nd(&m.b, C::kGradX ? a.dy : a.x, type, esize, 2, C::kGradX ? Y : X, box_r) &&
+           make_map_nd(&m.whole, C::kGradX ? a.dy : a.x, type, esize, 2, C::kGradX ? Y : X, box_b);
     }
   }
-  if (C::kGradW) {
-    const int box_o[3] = {kBM, kOutCols, 1};
-    ok = ok && make_map_nd(&m.out, a.o, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, 3, W, box_o,
-                           CU_TENSOR_MAP_SWIZZLE_NONE);
-  }
+  const int box_o[3] = {kBM, kOutCols, 1};
+  const int64_t O[2] = {C::kGradX ? a.in : a.out, a.g.M};
+  ok = ok && make_map_nd(&m.out, a.o,
+                         F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                         C::kOutSize, C::kGradW ? 3 : 2, C::kGradW ? W : O, box_o,
+                         CU_TENSOR_MAP_SWIZZLE_NONE);
   if (!ok) return cudaErrorInvalidValue;
   int dev = 0, sms = 148;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   const size_t fixed = 1024 + C::kOut + sizeof(GroupTab) * static_cast<size_t>(a.g.G);
-  const size_t statics = sizeof(GroupScratch) + (2 * kMaxStages + 5) * 8 + 64;
+  const size_t statics = sizeof(GroupScratch) + (3 * kMaxStages + 5) * 8 + 64;
   int stages = static_cast<int>((kSmemLimit - statics - fixed) / C::kStage);
   if (stages > kMaxStages) stages = kMaxStages;
   const size_t smem = fixed + static_cast<size_t>(stages) * C::kStage;
-  auto kernel = k_linear_tc<P, CTAS, BN, PIECES>;
+  auto kernel = k_linear_tc<P, CTAS, BN, F32>;
   OMNI_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 static_cast<int>(smem)));
   // no more pairs (or CTAs) than there can be tiles
@@ -925,16 +990,16 @@ cudaError_t launch(const LinearArgs& a, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-template <Product P, bool PIECES>
+template <Product P, bool F32>
 cudaError_t pick(const LinearArgs& a, cudaStream_t s) {
   const int64_t live = a.g.G < a.g.M ? a.g.G : a.g.M;
   const int64_t each = (a.g.M + live - 1) / live;  // rows of a group, on average
   const int rule = each <= 32 ? 32 : each <= 64 ? 64 : each <= 128 ? 128 : 256;
   int v = rule;
-  if (v == 32) return launch<P, 1, 32, PIECES>(a, s);
-  if (v == 64) return launch<P, 1, 64, PIECES>(a, s);
-  if (v == 128) return launch<P, 1, 128, PIECES>(a, s);
-  return launch<P, 2, 256, PIECES>(a, s);
+  if (v == 32) return launch<P, 1, 32, F32>(a, s);
+  if (v == 64) return launch<P, 1, 64, F32>(a, s);
+  if (v == 128) return launch<P, 1, 128, F32>(a, s);
+  return launch<P, 2, 256, F32>(a, s);
 }
 
 }  // namespace
@@ -949,7 +1014,8 @@ cudaError_t launch_linear(Product p, const LinearArgs& a, cudaStream_t s) {
       return f32 ? pick<Product::kGradX, true>(a, s) : pick<Product::kGradX, false>(a, s);
     case Product::kGradW:
       return launch<Product::kGradW, 2, 256, true>(a, s);
-    default: return pick<Product::kInt8, false>(a, s);
+    default:
+      return f32 ? pick<Product::kInt8, true>(a, s) : pick<Product::kInt8, false>(a, s);
   }
 }
 
