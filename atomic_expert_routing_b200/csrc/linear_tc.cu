@@ -656,7 +656,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        if (!ok) {
+        if (ok) {
+          // every MMA's arrival on a stage's barrier has come, the other CTA's
+          // too, before this CTA may exit
+          for (uint32_t k = issued > static_cast<uint32_t>(stages) ? issued - stages : 0u;
+               k < issued; ++k)
+            wait_for<false>(empty0 + 8 * (k % stages), (k / stages) & 1, a.status);
+        } else {
           // a wait timed out: the loads in flight land (each wait bounded again)
           // before the CTA exits
           if (C::kGradW)
@@ -751,7 +757,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         raise_status(a.status, OMNI_DEV_BAD_INDEX);
         return 0;
       };
-      auto wait_empty = [&](uint32_t no, int* s) -> bool {  // stage number no
+      // Stage number no.  A warp waits for every kRowWarps-th stage only; with at
+      // least that many stages in the ring, the wait before told it that the
+      // barrier is at most one phase behind, so the parity is not mistaken.
+      auto wait_empty = [&](uint32_t no, int* s) -> bool {
         *s = static_cast<int>(no % stages);
         const uint32_t ph = (no / stages) & 1;
         return __all_sync(0xffffffffu, wait_for<false>(empty0 + 8 * *s, ph ^ 1, a.status));
@@ -827,7 +836,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               copies_arrive(full0 + 8 * s);
             }
-          } else if (tail && ((no + blocks - 1) & (kRowWarps - 1)) == mine) {
+          } else if (tail && mine == 0) {
+            // one warp takes every such block, in order: it is then never more
+            // than one phase from a tail barrier's, and its parity says which
             zero_tail();
             __syncwarp();
             if (ok && lane == 0) {  // in place of the loads' two expects
@@ -962,6 +973,7 @@ cudaError_t launch(const LinearArgs& a, cudaStream_t s) {
   const size_t statics = sizeof(GroupScratch) + (3 * kMaxStages + 5) * 8 + 64;
   int stages = static_cast<int>((kSmemLimit - statics - fixed) / C::kStage);
   if (stages > kMaxStages) stages = kMaxStages;
+  if (stages < kRowWarps) return cudaErrorInvalidConfiguration;  // (no case: see wait_empty)
   const size_t smem = fixed + static_cast<size_t>(stages) * C::kStage;
   auto kernel = k_linear_tc<P, CTAS, BN, F32>;
   OMNI_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,

@@ -64,6 +64,8 @@ SHAPES = [
     ([700, 3], 512, 264, 2),
     ([2, 1300, 0, 255, 256], 520, 520, 0),
     ([5] * 70, 128, 256, 3),
+    # several tiles to a CTA, most groups ending inside a block of 64 and of 16 rows
+    ([1 + 37 * q % 83 for q in range(60)], 520, 1032, 0),
 ]
 IDS = [f"{len(s[0])}x{sum(s[0])}-{s[1]}-{s[2]}" for s in SHAPES]
 
