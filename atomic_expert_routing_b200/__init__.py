@@ -505,37 +505,40 @@ def _out_code(name, dtype):
     return code
 
 
-def _address(name, t, dev):
-    """A tensor's address for the library (None: no tensor).  The calls below
-    are short enough that the binding's own time counts: plain integers."""
-    if t is None:
-        return None
-    if t.device != dev:
-        raise ValueError(f"{name}: on {t.device}, the call's first tensor is on {dev}")
-    if not t.is_cuda:
-        raise ValueError("tensors passed to the CUDA library must live on a CUDA device")
-    if not t.is_contiguous():
-        raise ValueError("tensors passed to the CUDA library must be contiguous")
-    return t.data_ptr()
+def _addresses(index, *named):
+    """The addresses of (name, tensor or None) pairs, every tensor contiguous on
+    CUDA device `index`.  A decode batch's products take some ten microseconds:
+    the binding's own time counts, so a tensor is asked three things only."""
+    out = []
+    for name, t in named:
+        if t is None:
+            out.append(None)
+            continue
+        if t.get_device() != index or not t.is_contiguous():
+            if not t.is_cuda:
+                raise ValueError("tensors passed to the CUDA library must live on a CUDA device")
+            if t.get_device() != index:
+                raise ValueError(f"{name}: on {t.device}, the call's first tensor is on "
+                                 f"cuda:{index}")
+            raise ValueError("tensors passed to the CUDA library must be contiguous")
+        out.append(t.data_ptr())
+    return out
 
 
 def _linear_dims(names, x, W, group_off, ids, n_groups, rows, counts, dtype):
     """The checks the grouped products share, and the dims of a call of
     x [T, in] with W [E, out, in] of the given dtype."""
     i32 = torch.int32
-    if x.dtype != dtype:
-        raise ValueError(f"{names[0]}: dtype {x.dtype}, the call reads {dtype}")
-    if W.dtype != dtype:
-        raise ValueError(f"{names[1]}: dtype {W.dtype}, the call reads {dtype}")
-    if x.dim() != 2:
-        raise ValueError(f"{names[0]}: {x.dim()} dimensions, the call reads 2")
-    if W.dim() != 3:
-        raise ValueError(f"{names[1]}: {W.dim()} dimensions, the call reads 3")
+    for name, t, nd in ((names[0], x, 2), (names[1], W, 3)):
+        if t.dtype != dtype:
+            raise ValueError(f"{name}: dtype {t.dtype}, the call reads {dtype}")
+        if t.dim() != nd:
+            raise ValueError(f"{name}: {t.dim()} dimensions, the call reads {nd}")
     T, n_in = x.shape
     E, n_out, w_in = W.shape
     if n_in != w_in:
         raise ValueError(f"{names[0]}: rows of {n_in} elements, {names[1]} takes {w_in}")
-    G = 1
+    G, M = 1, T
     if group_off is not None:
         _expect("group_off", group_off, 2, i32)
         G = group_off.numel() - 1
@@ -545,21 +548,31 @@ def _linear_dims(names, x, W, group_off, ids, n_groups, rows, counts, dtype):
         _expect("n_groups", n_groups, 1, i32)
     if rows is not None:
         _expect("rows", rows, 0, i32)
+        M = rows.numel()
     if counts is not None:
         _expect("counts", counts, 4, i32)
-    return _lib.LinearDims(T if rows is None else rows.numel(), T, n_in, n_out, E, G)
+    return _lib.LinearDims(M, T, n_in, n_out, E, G)
 
 
-def _run(fn, dev, stream, *args):
-    """A library call on stream (default: the current one of dev), with dev current."""
+def _index(t):
+    """The CUDA device index of a call's first tensor."""
+    if not t.is_cuda:
+        raise ValueError("tensors passed to the CUDA library must live on a CUDA device")
+    return t.get_device()
+
+
+def _run(fn, index, stream, *args):
+    """A library call on stream (default: the current one of device `index`),
+    with that device current."""
     lib = _lib.load()
-    s = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
-    if torch.cuda.current_device() == dev.index:
+    s = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == index:
         code = getattr(lib, fn)(*args, s)
     else:
-        with torch.cuda.device(dev):
+        with torch.cuda.device(index):
             code = getattr(lib, fn)(*args, s)
-    _lib.check(fn, code)
+    if code:
+        _lib.check(fn, code)
 
 
 def _linear_out(name, t, like, M, width, dtype):
@@ -582,14 +595,13 @@ def grouped_linear(x, W, group_off, *, ids=None, n_groups=None, rows=None, silu=
     y [M, out] in out_dtype (bf16 or fp32; of the given y, its own); rows in no group are
     left as they were."""
     D = _linear_dims(("x", "W"), x, W, group_off, ids, n_groups, rows, counts, torch.bfloat16)
-    dev = x.device
     y, D.out_dtype = _linear_out("y", y, x, D.M, D.out, out_dtype)
     if silu:
         D.flags = OMNI_LINEAR_SILU
-    _run("omni_grouped_linear", dev, stream, C.byref(D), _address("x", x, dev),
-         _address("W", W, dev), _address("group_off", group_off, dev), _address("ids", ids, dev),
-         _address("n_groups", n_groups, dev), _address("rows", rows, dev),
-         _address("y", y, dev), _address("counts", counts, dev))
+    index = _index(x)
+    _run("omni_grouped_linear", index, stream, C.byref(D),
+         *_addresses(index, ("x", x), ("W", W), ("group_off", group_off), ("ids", ids),
+                     ("n_groups", n_groups), ("rows", rows), ("y", y), ("counts", counts)))
     return y
 
 
@@ -603,7 +615,6 @@ def grouped_linear_backward(x, W, dy, group_off, *, ids=None, n_groups=None, row
     no group are left as they were either way); without one, a new dW holds zeros there.
     Returns a dict of those asked for."""
     D = _linear_dims(("x", "W"), x, W, group_off, ids, n_groups, rows, counts, torch.bfloat16)
-    dev = x.device
     _expect("dy", dy, D.M * D.out, torch.bfloat16)
     if not (need_dx or need_dW):
         raise ValueError("need_dx and need_dW: no gradient asked for")
@@ -615,16 +626,16 @@ def grouped_linear_backward(x, W, dy, group_off, *, ids=None, n_groups=None, row
             # with ids or n_groups some matrices may be in no group
             make = torch.empty if ids is None and n_groups is None and D.G == D.E \
                 else torch.zeros
-            g["dW"], accumulate = make(W.shape, dtype=torch.float32, device=dev), False
+            g["dW"], accumulate = make(W.shape, dtype=torch.float32, device=W.device), False
         else:
             _expect("dW", dW, W.numel(), torch.float32)
             g["dW"] = dW
-    _run("omni_grouped_linear_backward", dev, stream, C.byref(D), _address("x", x, dev),
-         _address("W", W, dev), _address("dy", dy, dev), _address("group_off", group_off, dev),
-         _address("ids", ids, dev), _address("n_groups", n_groups, dev),
-         _address("rows", rows, dev), _address("dx", g.get("dx"), dev),
-         _address("dW", g.get("dW"), dev), 1 if accumulate else 0,
-         _address("counts", counts, dev))
+    index = _index(x)
+    _run("omni_grouped_linear_backward", index, stream, C.byref(D),
+         *_addresses(index, ("x", x), ("W", W), ("dy", dy), ("group_off", group_off),
+                     ("ids", ids), ("n_groups", n_groups), ("rows", rows), ("dx", g.get("dx")),
+                     ("dW", g.get("dW"))),
+         1 if accumulate else 0, *_addresses(index, ("counts", counts)))
     return g
 
 
@@ -640,13 +651,13 @@ def quantize_rows(x, *, q=None, scale=None, stream=None):
     n = x.numel() // max(width, 1)
     _expect("q", q, x.numel(), torch.int8, optional=True)
     _expect("scale", scale, n, torch.float32, optional=True)
-    dev = x.device
     if q is None:
-        q = torch.empty_like(x, dtype=torch.int8, memory_format=torch.contiguous_format)
+        q = x.new_empty(x.shape, dtype=torch.int8)
     if scale is None:
         scale = x.new_empty(x.shape[:-1], dtype=torch.float32)
-    _run("omni_quantize_rows", dev, stream, n, width, code, _address("x", x, dev),
-         _address("q", q, dev), _address("scale", scale, dev))
+    index = _index(x)
+    _run("omni_quantize_rows", index, stream, n, width, code,
+         *_addresses(index, ("x", x), ("q", q), ("scale", scale)))
     return q, scale
 
 
@@ -664,17 +675,16 @@ def quantized_linear(xq, xs, Wq, Ws, group_off=None, *, ids=None, n_groups=None,
             raise ValueError("group_off is required with ids or n_groups")
         Wq = Wq.unsqueeze(0)
     D = _linear_dims(("xq", "Wq"), xq, Wq, group_off, ids, n_groups, rows, counts, torch.int8)
-    dev = xq.device
     _expect("xs", xs, D.T, torch.float32)
     _expect("Ws", Ws, D.E * D.out, torch.float32)
     y, D.out_dtype = _linear_out("y", y, xq, D.M, D.out, out_dtype)
     if silu:
         D.flags = OMNI_LINEAR_SILU
-    _run("omni_quantized_linear", dev, stream, C.byref(D), _address("xq", xq, dev),
-         _address("xs", xs, dev), _address("Wq", Wq, dev), _address("Ws", Ws, dev),
-         _address("group_off", group_off, dev), _address("ids", ids, dev),
-         _address("n_groups", n_groups, dev), _address("rows", rows, dev),
-         _address("y", y, dev), _address("counts", counts, dev))
+    index = _index(xq)
+    _run("omni_quantized_linear", index, stream, C.byref(D),
+         *_addresses(index, ("xq", xq), ("xs", xs), ("Wq", Wq), ("Ws", Ws),
+                     ("group_off", group_off), ("ids", ids), ("n_groups", n_groups),
+                     ("rows", rows), ("y", y), ("counts", counts)))
     return y
 
 

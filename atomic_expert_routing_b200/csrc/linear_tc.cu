@@ -28,6 +28,8 @@
 // error of about 1.1e-9 of the result per term of k.  bf16 results do not
 // show it; fp32 results are summed in pieces of 512 terms, which the draining
 // warps add up in registers, rounded to nearest.
+#include <atomic>
+
 #include "linear.cuh"
 #include "tc_common.cuh"
 
@@ -388,7 +390,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const bool halves = gathers;
   if (threadIdx.x == 32 * kLoadWarp) {
     prefetch_map(&maps.a);
-    prefetch_map(&maps.b);
+    if (C::kGradW) prefetch_map(&maps.b);
+    else if (!gathers) prefetch_map(&maps.whole);
     // A stage is full after its loads' two expects.  With gathered rows it is
     // one expect, the threads of one row warp, and in a pair's first CTA the
     // second's word that its half is ready.  Where dW has rows to zero, the
@@ -641,7 +644,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               } else if constexpr (C::kGradW) {
                 for (int h = 0; h < boxes; ++h)
                   load_2d<CTAS>(db + h * 8192, &maps.b, bar, j0 + 64 * h, tl.row0 + k);
-              } else if (nb == C::kNb) {
+              } else if (C::kBox == C::kNb || nb == C::kNb) {
                 load_2d<CTAS>(db, &maps.whole, bar, k, tl.row0 + j0);
               } else {
                 for (int q = 0; q < boxes; ++q)
@@ -745,6 +748,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the stages in turn, one each: a stage costs a warp some 650 cycles of
       // waits, arrival and bookkeeping beside its copies (16 bytes a thread,
       // eight threads to a row's 128 bytes, four rows at a time).
+      // (Two warps to a stage, which halves the time from a free stage to its last
+      // copy, is slower: 216 against 187 us at 16384 x 2048 x 4096.)
       const int mine = warp - kRowWarp;
       const int sub = lane >> 3, piece = lane & 7;
       // where the copy of row 4 q + sub goes: even and odd q (swizzled)
@@ -865,8 +870,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int h = 0; h < (C::kNb + 31) / 32; ++h)
             at[h] = 32 * h + lane < there ? checked(a.rows[row0 + 32 * h + lane]) : 0;
-          for (int kb = static_cast<int>((mine - no) & (kRowWarps - 1)); kb < blocks;
-               kb += kRowWarps) {
+          for (int kb = static_cast<int>((mine - no) & (kRowWarps - 1)); kb < blocks; kb += kRowWarps) {
             int s;
             ok = wait_empty(no + kb, &s);
             if (!ok) break;
@@ -877,7 +881,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               const uint32_t to = sB + s * C::kStageB + u * C::kBBytes;
               const int64_t c = static_cast<int64_t>(k) * (C::kI8 ? 1 : 2) + 16 * piece;  // bytes
               const char* xc = x + c;
-              if (k + C::kBlockK <= tl.K) {
+              if (k + C::kBlockK <= tl.K && nb == C::kNb) {
+#pragma unroll
+                for (int q = 0; q < C::kNb / 4; ++q) {
+                  const int row = __shfl_sync(0xffffffffu, at[q / 8], (4 * q + sub) & 31);
+                  copy16(to + q * 512 + (q & 1 ? odd : even), xc + row * pitch);
+                }
+              } else if (k + C::kBlockK <= tl.K) {
 #pragma unroll
                 for (int q = 0; q < C::kNb / 4; ++q)
                   if (4 * q < nb) {
@@ -939,7 +949,7 @@ bool make_map_nd(CUtensorMap* m, const void* base, CUtensorMapDataType type, int
 }
 
 template <Product P, int CTAS, int BN, bool F32>
-cudaError_t launch(const LinearArgs& a, cudaStream_t s) {
+cudaError_t launch(const LinearArgs& a, int sms, cudaStream_t s) {
   using C = Cfg<P, CTAS, BN, F32>;
   Maps m{};
   const int64_t W[3] = {a.in, a.out, a.g.E}, X[2] = {a.in, a.T}, Y[2] = {a.out, a.g.M};
@@ -954,21 +964,25 @@ cudaError_t launch(const LinearArgs& a, cudaStream_t s) {
       ok = make_map_nd(&m.a, a.x, type, esize, 2, X, box_64) &&
            make_map_nd(&m.b, a.dy, type, esize, 2, Y, box_64);
     } else {
-      ok = make_map_nd(&m.a, a.W, type, esize, 3, W, box_w) &&
-           make_map_nd(&m.b, C::kGradX ? a.dy : a.x, type, esize, 2, C::kGradX ? Y : X, box_r) &&
-           make_map_nd(&m.whole, C::kGradX ? a.dy : a.x, type, esize, 2, C::kGradX ? Y : X, box_b);
+      // (gathered rows need no map; a box of all of a tile's columns and one of
+      // some are the same where tiles are narrow)
+      ok = make_map_nd(&m.a, a.W, type, esize, 3, W, box_w);
+      if (C::kGradX || a.rows == nullptr) {
+        const void* b = C::kGradX ? a.dy : a.x;
+        const int64_t* dim = C::kGradX ? Y : X;
+        ok = ok && make_map_nd(&m.whole, b, type, esize, 2, dim, box_b);
+        if (C::kBox < C::kNb) ok = ok && make_map_nd(&m.b, b, type, esize, 2, dim, box_r);
+      }
     }
   }
   const int box_o[3] = {kBM, kOutCols, 1};
   const int64_t O[2] = {C::kGradX ? a.in : a.out, a.g.M};
-  ok = ok && make_map_nd(&m.out, a.o,
-                         F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                         C::kOutSize, C::kGradW ? 3 : 2, C::kGradW ? W : O, box_o,
-                         CU_TENSOR_MAP_SWIZZLE_NONE);
+  if (C::kGradW || a.g.M >= kOutCols)  // (fewer rows have no whole chunk)
+    ok = ok && make_map_nd(&m.out, a.o,
+                           F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                           C::kOutSize, C::kGradW ? 3 : 2, C::kGradW ? W : O, box_o,
+                           CU_TENSOR_MAP_SWIZZLE_NONE);
   if (!ok) return cudaErrorInvalidValue;
-  int dev = 0, sms = 148;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   const size_t fixed = 1024 + C::kOut + sizeof(GroupTab) * static_cast<size_t>(a.g.G);
   const size_t statics = sizeof(GroupScratch) + (3 * kMaxStages + 5) * 8 + 64;
   int stages = static_cast<int>((kSmemLimit - statics - fixed) / C::kStage);
@@ -976,8 +990,16 @@ cudaError_t launch(const LinearArgs& a, cudaStream_t s) {
   if (stages < kRowWarps) return cudaErrorInvalidConfiguration;  // (no case: see wait_empty)
   const size_t smem = fixed + static_cast<size_t>(stages) * C::kStage;
   auto kernel = k_linear_tc<P, CTAS, BN, F32>;
-  OMNI_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                static_cast<int>(smem)));
+  int dev = 0;
+  cudaGetDevice(&dev);
+  // once per device (of a bit each; later devices are asked every time)
+  static std::atomic<uint64_t> allowed{0};
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if ((allowed.load(std::memory_order_relaxed) & bit) == 0) {
+    OMNI_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  static_cast<int>(kSmemLimit - statics)));
+    allowed.fetch_or(bit, std::memory_order_relaxed);
+  }
   // no more pairs (or CTAs) than there can be tiles
   const int64_t mt = ((C::kMnA ? a.in : a.out) + kBM * CTAS - 1) / (kBM * CTAS);
   const int64_t live = a.g.G < a.g.M ? a.g.G : a.g.M;
@@ -1002,32 +1024,89 @@ cudaError_t launch(const LinearArgs& a, cudaStream_t s) {
   return cudaGetLastError();
 }
 
+// Which tiles a product takes.  Measured on 16384 rows, 2048 to 4096 wide, a
+// k-block of 128 bytes costs a slot (an SM, or a pair) about
+//   32 wide 305 cycles, 64: 374, 128: 540, pairs of 256: 740;
+// a tile with fewer columns costs in proportion, down to what loading its A
+// and turning a stage over cost.  The estimate is the rounds the slots need for groups of equal size
+// times the mean cost of a tile; the cheapest is taken.  A batch with many
+// rows per group ends up with pairs of 256 (1550 TFLOP/s against 1090 at
+// 128), a decode batch with 32, and a product with few tiles with narrower
+// ones than its rows would fill, so that more SMs have one (300 rows, 2048 to
+// 512: 40 tiles of 32 in 305 cycles a block against 4 pairs in 740).
+struct Shape {
+  int ctas, bn, cycles, least;
+};
+constexpr Shape kShapes[] = {
+    {1, 32, 305, 305}, {1, 64, 374, 330}, {1, 128, 540, 420}, {2, 256, 740, 480}};
+
+int64_t round_cost(const Shape& sh, int64_t I, int64_t rows, int64_t live, int sms) {
+  const int64_t each = (rows + live - 1) / live;  // rows of a group
+  const int64_t full = each / sh.bn, rest = each % sh.bn;
+  int64_t cost = full * sh.cycles;
+  if (rest > 0) {
+    const int64_t part = sh.cycles * rest / sh.bn;
+    cost += part > sh.least ? part : sh.least;
+  }
+  const int64_t per = full + (rest > 0 ? 1 : 0), slots = sms / sh.ctas;
+  const int64_t tiles = live * per * ((I + kBM * sh.ctas - 1) / (kBM * sh.ctas));
+  return (tiles + slots - 1) / slots * cost / per;
+}
+
 template <Product P, bool F32>
-cudaError_t pick(const LinearArgs& a, cudaStream_t s) {
+cudaError_t pick(const LinearArgs& a, int sms, cudaStream_t s) {
   const int64_t live = a.g.G < a.g.M ? a.g.G : a.g.M;
-  const int64_t each = (a.g.M + live - 1) / live;  // rows of a group, on average
-  const int rule = each <= 32 ? 32 : each <= 64 ? 64 : each <= 128 ? 128 : 256;
-  int v = rule;
-  if (v == 32) return launch<P, 1, 32, F32>(a, s);
-  if (v == 64) return launch<P, 1, 64, F32>(a, s);
-  if (v == 128) return launch<P, 1, 128, F32>(a, s);
-  return launch<P, 2, 256, F32>(a, s);
+  int best = 0;
+  int64_t least = 0;
+  for (int q = 0; q < 4; ++q) {
+    const int64_t c =
+        round_cost(kShapes[q], P == Product::kGradX ? a.in : a.out, a.g.M, live, sms);
+    if (q == 0 || c < least) {
+      best = q;
+      least = c;
+    }
+  }
+  switch (best) {
+    case 0: return launch<P, 1, 32, F32>(a, sms, s);
+    case 1: return launch<P, 1, 64, F32>(a, sms, s);
+    case 2: return launch<P, 1, 128, F32>(a, sms, s);
+    default: return launch<P, 2, 256, F32>(a, sms, s);
+  }
+}
+
+// dW: pairs of 256 x 256, or single CTAs of 128 x 128 where those leave a
+// third or more of a pair's columns idle or give the SMs fewer rounds.  A tile
+// costs its products (740 or 540 cycles per 64 rows) or its way out (4500 or
+// 2300), whichever is more.
+cudaError_t pick_grad_w(const LinearArgs& a, int sms, cudaStream_t s) {
+  const int64_t blocks = (a.g.M / a.g.G + 63) / 64;
+  auto cost = [&](int64_t m, int64_t n, int64_t slots, int64_t block, int64_t out) {
+    const int64_t tiles = (a.in + m - 1) / m * ((a.out + n - 1) / n) * a.g.G;
+    return (tiles + slots - 1) / slots * (blocks * block > out ? blocks * block : out);
+  };
+  bool pairs = cost(256, 256, sms / 2, 740, 4500) <= cost(128, 128, sms, 540, 2300);
+  return pairs ? launch<Product::kGradW, 2, 256, true>(a, sms, s)
+               : launch<Product::kGradW, 1, 128, true>(a, sms, s);
 }
 
 }  // namespace
 
 cudaError_t launch_linear(Product p, const LinearArgs& a, cudaStream_t s) {
   if (encode_fn() == nullptr) return cudaErrorNotSupported;
+  int dev = 0, sms = 148;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   const bool f32 = a.out_f32 != 0;
   switch (p) {
     case Product::kForward:
-      return f32 ? pick<Product::kForward, true>(a, s) : pick<Product::kForward, false>(a, s);
+      return f32 ? pick<Product::kForward, true>(a, sms, s)
+                 : pick<Product::kForward, false>(a, sms, s);
     case Product::kGradX:
-      return f32 ? pick<Product::kGradX, true>(a, s) : pick<Product::kGradX, false>(a, s);
-    case Product::kGradW:
-      return launch<Product::kGradW, 2, 256, true>(a, s);
+      return f32 ? pick<Product::kGradX, true>(a, sms, s)
+                 : pick<Product::kGradX, false>(a, sms, s);
+    case Product::kGradW: return pick_grad_w(a, sms, s);
     default:
-      return f32 ? pick<Product::kInt8, true>(a, s) : pick<Product::kInt8, false>(a, s);
+      return f32 ? pick<Product::kInt8, true>(a, sms, s) : pick<Product::kInt8, false>(a, sms, s);
   }
 }
 

@@ -1,37 +1,33 @@
 // Rows to 8-bit integers with one scale each:
 //   scale = fp32(max|x| / 127),  q = the integer nearest to x / scale.
 // A row is read once and kept in registers between its maximum and its
-// integers, by a warp (rows of up to 2048 values, when there are many) or by
-// a CTA of eight warps (up to 16384 values; a decode batch's few rows would
-// leave most of the GPU idle with a warp each); longer rows are read twice.
+// integers, by two warps (rows of up to 2048 values, when there are many) or
+// by a CTA of eight (up to 16384 values; a decode batch's few rows would leave
+// most of the GPU idle with a warp each); longer rows are read twice.
 //
 // The quotient is rounded exactly, as if formed in infinite precision: the
 // fp32 quotient can land on the middle between two integers when the true
-// one lies beside it, so a quotient that comes within 10^-4 of a middle is
-// checked against x with fused multiply-adds, whose sign is that of the
-// exact difference.
+// one lies beside it, so quotients within 3e-5 of a middle are checked
+// against x with fused multiply-adds, whose sign is that of the exact
+// difference.
 #include "linear.cuh"
 
 namespace omni {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kHeld = 8;  // vectors of 8 values a thread keeps
 
 // |v|'s bits, monotone in |v|, with every NaN above infinity
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
 // The integer nearest to x / s (ties to even), clamped to [-127, 127];
-// |x| <= 191 s, s normal.  x * inv is off by less than 10^-4 from x / s.
+// |x| <= 191 s, s normal.
 __device__ __forceinline__ int nearest_quotient(float x, float s, float inv) {
-  const float t = x * inv;
-  float q = rintf(t);
-  if (fabsf(t - q) > 0.4999f) {
-    const float up = fmaf(-(q + 0.5f), s, x), down = fmaf(-(q - 0.5f), s, x);
-    const bool odd = (static_cast<int>(q) & 1) != 0;
-    if (up > 0.0f || (up == 0.0f && odd)) q += 1.0f;
-    else if (down < 0.0f || (down == 0.0f && odd)) q -= 1.0f;
-  }
+  float q = rintf(x * inv);  // at most one off
+  const float up = fmaf(-(q + 0.5f), s, x), down = fmaf(-(q - 0.5f), s, x);
+  const bool odd = (static_cast<int>(q) & 1) != 0;
+  if (up > 0.0f || (up == 0.0f && odd)) q += 1.0f;
+  else if (down < 0.0f || (down == 0.0f && odd)) q -= 1.0f;
   return static_cast<int>(fminf(fmaxf(q, -127.0f), 127.0f));
 }
 
@@ -50,19 +46,8 @@ __device__ __forceinline__ RowScale row_scale(uint32_t m, float* scale, bool sto
   // tiny rows are scaled up (exactly) so that the differences stay normal
   r.lift = s < 0x1p-80f ? 0x1p100f : 1.0f;
   r.s = s * r.lift;
-  r.inv = __fdiv_rn(1.0f, r.s);
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r.inv) : "f"(r.s));  // within 2^-23
   return r;
-}
-
-__device__ __forceinline__ uint2 quantize8(const float* f, const RowScale& r) {
-  uint32_t w[2] = {0u, 0u};
-  if (!r.zero) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      w[i >> 2] |= (static_cast<uint32_t>(nearest_quotient(f[i] * r.lift, r.s, r.inv)) & 0xffu)
-                   << (8 * (i & 3));
-  }
-  return make_uint2(w[0], w[1]);
 }
 
 // eight values as loaded
@@ -72,6 +57,12 @@ template <> struct Eight<__nv_bfloat16> {
   __device__ __forceinline__ void load(const __nv_bfloat16* p) {
     u = *reinterpret_cast<const uint4*>(p);
   }
+  // the largest |value|'s bits as a float's; m is of the same kind
+  __device__ __forceinline__ uint32_t largest(uint32_t m) const {
+    const uint32_t k = 0x7fff7fffu;
+    const uint32_t w = __vmaxu2(__vmaxu2(u.x & k, u.y & k), __vmaxu2(u.z & k, u.w & k));
+    return max(m, max(w << 16, w & 0xffff0000u));
+  }
   __device__ __forceinline__ void get(float* f) const {
     f[0] = bf16lo(u.x); f[1] = bf16hi(u.x); f[2] = bf16lo(u.y); f[3] = bf16hi(u.y);
     f[4] = bf16lo(u.z); f[5] = bf16hi(u.z); f[6] = bf16lo(u.w); f[7] = bf16hi(u.w);
@@ -80,14 +71,70 @@ template <> struct Eight<__nv_bfloat16> {
 template <> struct Eight<float> {
   float v[8];
   __device__ __forceinline__ void load(const float* p) { load8(p, v); }
+  __device__ __forceinline__ uint32_t largest(uint32_t m) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[i]));
+    return m;
+  }
   __device__ __forceinline__ void get(float* f) const {
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[i] = v[i];
   }
 };
 
-// TPR threads per row (32 or the CTA); HELD: the row fits their registers
-template <typename T, int TPR, bool HELD>
+constexpr float kRound = 12582912.0f;  // 1.5 * 2^23
+constexpr float kNear = 0.49997f;
+
+__device__ __forceinline__ uint2 pack8(const uint32_t* q) {
+  return make_uint2(
+      __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410),
+      __byte_perm(__byte_perm(q[4], q[5], 0x0040), __byte_perm(q[6], q[7], 0x0040), 0x5410));
+}
+
+// The same with every doubtful value done exactly.  One copy of it, not one per
+// vector a thread holds: inlined, the kernel waited on its instructions (36 us
+// for 16384 x 2048 bf16).
+template <typename T>
+__device__ __noinline__ uint2 quantize8_exact(Eight<T> e, float s, float inv, float lift) {
+  float f[8];
+  e.get(f);
+  uint32_t q[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float t = f[i] * inv;
+    q[i] = __float_as_uint(__fadd_rn(t, kRound));
+    if (lift != 1.0f || fabsf(t - rintf(t)) > kNear)
+      q[i] = static_cast<uint32_t>(nearest_quotient(f[i] * lift, s, inv));
+  }
+  return pack8(q);
+}
+
+// Adding 1.5 * 2^23 rounds a small value to the nearest integer (ties to even)
+// and leaves the integer in the low bits.  x * inv, a value up to 127.5, is off
+// by at most 127.5 * (2^-23 + 2^-24) < 2.3e-5 from x / s, so a rounding that is
+// 3e-5 or more from the middle stands.  Nearer ones (among
+// bf16 values, all those of half the largest: some of a row of 2048) and
+// those of a scaled-up row (whose quotients may pass 127) are done exactly.
+template <typename T>
+__device__ __forceinline__ uint2 quantize8(const Eight<T>& e, const RowScale& r) {
+  float f[8];
+  e.get(f);
+  uint32_t q[8];
+  bool near = r.lift != 1.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float t = f[i] * r.inv;
+    const float m = __fadd_rn(t, kRound);
+    near |= fabsf(t - __fsub_rn(m, kRound)) > kNear;
+    q[i] = __float_as_uint(m);
+  }
+  if (r.zero) return make_uint2(0u, 0u);
+  return near ? quantize8_exact(e, r.s, r.inv, r.lift) : pack8(q);
+}
+
+// TPR threads per row, HELD vectors of 8 values of it in each thread's
+// registers (0: the row does not fit)
+template <typename T, int TPR, int HELD>
 __global__ void __launch_bounds__(kThreads)
     k_quantize_rows(int64_t n, int width, const T* __restrict__ src, int8_t* __restrict__ q,
                     float* __restrict__ scale) {
@@ -96,53 +143,41 @@ __global__ void __launch_bounds__(kThreads)
   pdl_trigger();
   const int lane = threadIdx.x % TPR;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * (kThreads / TPR) + threadIdx.x / TPR;
-  if (row >= n) return;
+  const bool there = row < n;
+  if (!there) width = 0;
   const T* p = src + row * width;
   int8_t* o = q + row * width;
-  Eight<T> held[HELD ? kHeld : 1];
+  Eight<T> held[HELD > 0 ? HELD : 1];
   uint32_t m = 0;
-  auto largest = [&](const Eight<T>& e) {
-    float f[8];
-    e.get(f);
+  if constexpr (HELD > 0) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, abs_bits(f[i]));
-  };
-  if constexpr (HELD) {
-#pragma unroll
-    for (int h = 0; h < kHeld; ++h)
+    for (int h = 0; h < HELD; ++h)
       if ((h * TPR + lane) * 8 < width) held[h].load(p + (h * TPR + lane) * 8);
 #pragma unroll
-    for (int h = 0; h < kHeld; ++h)
-      if ((h * TPR + lane) * 8 < width) largest(held[h]);
+    for (int h = 0; h < HELD; ++h)
+      if ((h * TPR + lane) * 8 < width) m = held[h].largest(m);
   } else {
     for (int c = lane * 8; c < width; c += TPR * 8) {
       held[0].load(p + c);
-      largest(held[0]);
+      m = held[0].largest(m);
     }
   }
   m = __reduce_max_sync(0xffffffffu, m);
-  if constexpr (TPR > 32) {
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
-    __syncthreads();
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
+  __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) m = max(m, part[w]);
-  }
-  const RowScale r = row_scale(m, scale + row, lane == 0);
-  float f[8];
-  if constexpr (HELD) {
+  for (int w = 0; w < TPR / 32; ++w) m = max(m, part[threadIdx.x / TPR * (TPR / 32) + w]);
+  const RowScale r = row_scale(m, scale + row, there && lane == 0);
+  if constexpr (HELD > 0) {
 #pragma unroll
-    for (int h = 0; h < kHeld; ++h) {
+    for (int h = 0; h < HELD; ++h) {
       const int c = (h * TPR + lane) * 8;
-      if (c < width) {
-        held[h].get(f);
-        *reinterpret_cast<uint2*>(o + c) = quantize8(f, r);
-      }
+      if (c < width) *reinterpret_cast<uint2*>(o + c) = quantize8(held[h], r);
     }
   } else {
     for (int c = lane * 8; c < width; c += TPR * 8) {
       held[0].load(p + c);
-      held[0].get(f);
-      *reinterpret_cast<uint2*>(o + c) = quantize8(f, r);
+      *reinterpret_cast<uint2*>(o + c) = quantize8(held[0], r);
     }
   }
 }
@@ -150,17 +185,18 @@ __global__ void __launch_bounds__(kThreads)
 template <typename T>
 cudaError_t launch(int64_t n, int width, const void* src, int8_t* q, float* scale,
                    cudaStream_t s) {
-  // a warp per row once that gives every SM a few CTAs
-  const bool warps = width <= 32 * 8 * kHeld && n >= 148 * 4 * (kThreads / 32);
-  const bool held = width <= kThreads * 8 * kHeld;
-  const unsigned grid = static_cast<unsigned>(warps ? (n + kThreads / 32 - 1) / (kThreads / 32) : n);
   const T* p = static_cast<const T*>(src);
-  if (warps)
-    OMNI_TRY(launch_k(k_quantize_rows<T, 32, true>, grid, kThreads, 0, s, n, width, p, q, scale));
-  else if (held)
-    OMNI_TRY(launch_k(k_quantize_rows<T, kThreads, true>, grid, kThreads, 0, s, n, width, p, q, scale));
+  auto go = [&](auto kernel, int rows_per_cta) -> cudaError_t {
+    const unsigned grid = static_cast<unsigned>((n + rows_per_cta - 1) / rows_per_cta);
+    return launch_k(kernel, grid, kThreads, 0, s, n, width, p, q, scale);
+  };
+  // two warps per row once that gives every SM a few CTAs
+  if (width <= 64 * 8 * 4 && n >= 148 * 4 * (kThreads / 64))
+    OMNI_TRY(go(k_quantize_rows<T, 64, 4>, kThreads / 64));
+  else if (width <= kThreads * 8 * 8)
+    OMNI_TRY(go(k_quantize_rows<T, kThreads, 8>, 1));
   else
-    OMNI_TRY(launch_k(k_quantize_rows<T, kThreads, false>, grid, kThreads, 0, s, n, width, p, q, scale));
+    OMNI_TRY(go(k_quantize_rows<T, kThreads, 0>, 1));
   return cudaGetLastError();
 }
 

@@ -319,7 +319,8 @@ def _quantize_ref(x):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
-@pytest.mark.parametrize("n,width", [(1, 16), (5, 48), (64, 2048), (1003, 1040), (3, 65536)])
+@pytest.mark.parametrize("n,width", [(1, 16), (5, 48), (64, 2048), (1003, 1040), (3, 65536),
+                                     (5001, 1040), (4999, 2048), (4800, 16)])
 def test_quantize_rows(n, width, dtype):
     g = _gen(8)
     x = torch.randn((n, width), generator=g, device="cuda")

@@ -182,3 +182,21 @@ def test_host_tensors_are_refused():
                                                OFF)):
         with pytest.raises(ValueError, match="CUDA device"):
             call()
+
+
+def test_register_split_of_the_product_kernels():
+    """The kernels move registers between their warps (setmaxnreg): the shares add up to what a
+    block of 512 threads starts with only if the compiler gives each thread exactly 128.  With
+    fewer, the draining warps would wait for registers that never come."""
+    import os
+    import re
+
+    src = os.path.join(libbuild.CSRC, "linear_tc.cu")
+    libbuild.build()
+    if not os.path.exists(libbuild.report(src)):
+        libbuild.build(force=True)
+    text = open(libbuild.report(src)).read()
+    used = re.findall(r"Used (\d+) registers", text)
+    assert len(used) > 20 and set(used) == {"128"}
+    spills = re.findall(r"(\d+) bytes spill stores, (\d+) bytes spill loads", text)
+    assert spills and all(s == ("0", "0") for s in spills)
