@@ -453,7 +453,7 @@ typedef struct omni_linear_dims {
  * an id outside [0, E) or not above every earlier id, or a group count
  * outside [0, G] (clamped) sets OMNI_DEV_BAD_INDEX, and the group is left
  * out (without ids its dW is that of a group without rows); so does an entry of rows outside [0, T), which is taken as row 0.
- * The calls need no workspace. */
+ * The calls need no workspace.  Outputs must not overlap any input. */
 
 /*
  * y[r] = x[rows[r]] . W[e]^T for every row r of the group of expert e, SiLU

@@ -294,6 +294,72 @@ def test_bad_rows_are_reported():
     assert torch.equal(y, y0) and torch.equal(b["dW"], dW0)
 
 
+def test_many_groups():
+    """The largest number of groups, many of them empty or of a few rows."""
+    g = _gen(40)
+    sizes = np.random.default_rng(41).integers(0, 7, 1024)
+    off, M = _i32(_off(sizes)), int(sizes.sum())
+    x, W, dy = _normal(g, M, 16), _normal(g, 1024, 24, 16), _normal(g, M, 24)
+    counts = omni.new_counts("cuda")
+    y = omni.grouped_linear(x, W, off, out_dtype=F32, counts=counts)
+    r = omni.grouped_linear_backward(x, W, dy, off, out_dtype=F32, counts=counts)
+    e = torch.repeat_interleave(torch.arange(1024, device="cuda"),
+                                torch.from_numpy(sizes).cuda())
+    X, Y, w = x.double(), dy.double(), W.double()[e]
+    _close(y, torch.einsum("mi,moi->mo", X, w),
+           16 * ULP * torch.einsum("mi,moi->mo", X.abs(), w.abs()))
+    _close(r["dx"], torch.einsum("mo,moi->mi", Y, w),
+           24 * ULP * torch.einsum("mo,moi->mi", Y.abs(), w.abs()))
+    outer = torch.einsum("mo,mi->moi", Y, X)
+    ref = torch.zeros((1024, 24, 16), dtype=torch.float64, device="cuda")
+    mag = ref.clone().index_add_(0, e, outer.abs())
+    _close(r["dW"], ref.index_add_(0, e, outer), 8 * ULP * mag)
+    assert counts.tolist() == [0, 0, 0, 0]
+
+
+def test_offsets_past_32_bits():
+    """Outputs and matrices of more than 2^31 elements: the last rows, the last expert."""
+    g = _gen(42)
+    M, n_out = 1_050_003, 2056
+    x, W = _normal(g, M, 8), _normal(g, 2, n_out, 8)
+    y = omni.grouped_linear(x, W, _i32([0, 5, M]))
+    ref = x[-40:].double() @ W[1].double().T
+    _close(y[-40:], ref, 8 * ULP * (x[-40:].double().abs() @ W[1].double().abs().T))
+    del y
+    W = torch.zeros((2060, 1024, 1024), dtype=BF, device="cuda")
+    W[2059] = _normal(g, 1024, 1024)
+    x, dy = _normal(g, 33, 1024), _normal(g, 33, 1024)
+    kw = {"ids": _i32([0, 2059])}
+    y = omni.grouped_linear(x, W, _i32([0, 1, 33]), out_dtype=F32, **kw)
+    w, X = W[2059].double(), x[1:].double()
+    _close(y[1:], X @ w.T, 1024 * ULP * (X.abs() @ w.abs().T))
+    dW = torch.zeros((2060, 1024, 1024), device="cuda")
+    omni.grouped_linear_backward(x, W, dy, _i32([0, 1, 33]), dW=dW, need_dx=False, **kw)
+    Y = dy[1:].double()
+    _close(dW[2059], Y.T @ X, 32 * ULP * (Y.abs().T @ X.abs()))
+    assert not bool(dW[1:2059].any())
+
+
+def test_backward_calls_in_a_row_add_up():
+    """dx and dW of a call may run side by side; calls behind one another may not.  On small
+    integers every sum is exact, so the total of many calls is too."""
+    g = _gen(43)
+    sizes = [3, 70, 0, 129, 1, 40]
+    off, M = _i32(_off(sizes)), sum(sizes)
+
+    def ints(*shape):
+        return torch.randint(-3, 4, shape, generator=g, device="cuda").to(BF)
+
+    x, W, dy = ints(M, 264), ints(6, 136, 264), ints(M, 136)
+    one = omni.grouped_linear_backward(x, W, dy, off, out_dtype=F32)
+    total = torch.zeros_like(one["dW"])
+    for _ in range(40):
+        r = omni.grouped_linear_backward(x, W, dy, off, dW=total, out_dtype=F32)
+        x2 = r["dx"].to(BF)  # the kernel behind reads dx
+        assert x2.shape == (M, 264)
+    assert torch.equal(total, 40 * one["dW"]) and torch.equal(r["dx"], one["dx"])
+
+
 def test_no_rows():
     W = torch.ones((3, 64, 64), dtype=BF, device="cuda")
     x = torch.empty((0, 64), dtype=BF, device="cuda")
