@@ -17,6 +17,7 @@ with one expert per group; ``quantize_rows`` and ``quantized_linear`` are the
 from __future__ import annotations
 
 import ctypes as C
+import struct
 from dataclasses import dataclass
 
 import torch
@@ -505,53 +506,32 @@ def _out_code(name, dtype):
     return code
 
 
-def _addresses(index, *named):
-    """The addresses of (name, tensor or None) pairs, every tensor contiguous on
-    CUDA device `index`.  A decode batch's products take some ten microseconds:
-    the binding's own time counts, so a tensor is asked three things only."""
+# The calls below take the GPU some ten microseconds for a decode batch: the binding's own time
+# counts, so their checks ask each tensor a few things only, sizes are packed without a ctypes
+# structure, and outputs are allocated with plain integers (a tuple of sizes costs 0.7 us more).
+_pack_linear_dims = struct.Struct("6q2i").pack  # omni_linear_dims
+
+
+def _misplaced(name, t, index):
+    """Raise for a tensor that is not contiguous on CUDA device `index`."""
+    if not t.is_cuda:
+        raise ValueError("tensors passed to the CUDA library must live on a CUDA device")
+    if t.get_device() != index:
+        raise ValueError(f"{name}: on {t.device}, the call's first tensor is on cuda:{index}")
+    raise ValueError("tensors passed to the CUDA library must be contiguous")
+
+
+def _addresses(index, names, tensors):
+    """The addresses of tensors (None: no tensor), contiguous on CUDA device `index`."""
     out = []
-    for name, t in named:
+    for t in tensors:
         if t is None:
             out.append(None)
-            continue
-        if t.get_device() != index or not t.is_contiguous():
-            if not t.is_cuda:
-                raise ValueError("tensors passed to the CUDA library must live on a CUDA device")
-            if t.get_device() != index:
-                raise ValueError(f"{name}: on {t.device}, the call's first tensor is on "
-                                 f"cuda:{index}")
-            raise ValueError("tensors passed to the CUDA library must be contiguous")
-        out.append(t.data_ptr())
+        elif t.get_device() == index and t.is_contiguous():
+            out.append(t.data_ptr())
+        else:
+            _misplaced(names[len(out)], t, index)
     return out
-
-
-def _linear_dims(names, x, W, group_off, ids, n_groups, rows, counts, dtype):
-    """The checks the grouped products share, and the dims of a call of
-    x [T, in] with W [E, out, in] of the given dtype."""
-    i32 = torch.int32
-    for name, t, nd in ((names[0], x, 2), (names[1], W, 3)):
-        if t.dtype != dtype:
-            raise ValueError(f"{name}: dtype {t.dtype}, the call reads {dtype}")
-        if t.dim() != nd:
-            raise ValueError(f"{name}: {t.dim()} dimensions, the call reads {nd}")
-    T, n_in = x.shape
-    E, n_out, w_in = W.shape
-    if n_in != w_in:
-        raise ValueError(f"{names[0]}: rows of {n_in} elements, {names[1]} takes {w_in}")
-    G, M = 1, T
-    if group_off is not None:
-        _expect("group_off", group_off, 2, i32)
-        G = group_off.numel() - 1
-    if ids is not None:
-        _expect("ids", ids, G, i32)
-    if n_groups is not None:
-        _expect("n_groups", n_groups, 1, i32)
-    if rows is not None:
-        _expect("rows", rows, 0, i32)
-        M = rows.numel()
-    if counts is not None:
-        _expect("counts", counts, 4, i32)
-    return _lib.LinearDims(M, T, n_in, n_out, E, G)
 
 
 def _index(t):
@@ -561,16 +541,50 @@ def _index(t):
     return t.get_device()
 
 
+def _linear_sizes(names, x, W, group_off, ids, n_groups, rows, counts, dtype):
+    """The checks the grouped products share, and the sizes (M, T, in, out, E, G) of a call of
+    x [T, in] with W [E, out, in] of the given dtype."""
+    i32 = torch.int32
+    if x.dtype != dtype:
+        raise ValueError(f"{names[0]}: dtype {x.dtype}, the call reads {dtype}")
+    if W.dtype != dtype:
+        raise ValueError(f"{names[1]}: dtype {W.dtype}, the call reads {dtype}")
+    sx, sw = x.shape, W.shape
+    if len(sx) != 2:
+        raise ValueError(f"{names[0]}: {len(sx)} dimensions, the call reads 2")
+    if len(sw) != 3:
+        raise ValueError(f"{names[1]}: {len(sw)} dimensions, the call reads 3")
+    T, n_in = sx
+    E, n_out, w_in = sw
+    if n_in != w_in:
+        raise ValueError(f"{names[0]}: rows of {n_in} elements, {names[1]} takes {w_in}")
+    G, M = 1, T
+    if group_off is not None:
+        G = group_off.numel() - 1
+        if G < 1 or group_off.dtype != i32:
+            _expect("group_off", group_off, 2, i32)
+    if ids is not None:
+        _expect("ids", ids, G, i32)
+    if n_groups is not None:
+        _expect("n_groups", n_groups, 1, i32)
+    if rows is not None:
+        _expect("rows", rows, 0, i32)
+        M = rows.numel()
+    if counts is not None:
+        _expect("counts", counts, 4, i32)
+    return M, T, n_in, n_out, E, G
+
+
 def _run(fn, index, stream, *args):
     """A library call on stream (default: the current one of device `index`),
     with that device current."""
-    lib = _lib.load()
+    call = getattr(_lib.load(), fn)
     s = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
     if torch.cuda.current_device() == index:
-        code = getattr(lib, fn)(*args, s)
+        code = call(*args, s)
     else:
         with torch.cuda.device(index):
-            code = getattr(lib, fn)(*args, s)
+            code = call(*args, s)
     if code:
         _lib.check(fn, code)
 
@@ -579,10 +593,16 @@ def _linear_out(name, t, like, M, width, dtype):
     """The output [M, width]: t if given (its dtype is the call's), else a new
     tensor of dtype beside like; and its dtype's code."""
     if t is None:
-        return like.new_empty((M, width), dtype=dtype), _out_code("out_dtype", dtype)
+        code = _out_code("out_dtype", dtype)
+        return torch.empty(M, width, dtype=dtype, device=like.device), code
     code = _out_code(name, t.dtype)
     _expect(name, t, M * width, t.dtype)
     return t, code
+
+
+_LINEAR_ARGS = ("x", "W", "group_off", "ids", "n_groups", "rows", "y", "counts")
+_BACKWARD_ARGS = ("x", "W", "dy", "group_off", "ids", "n_groups", "rows", "dx", "dW")
+_QUANTIZED_ARGS = ("xq", "xs", "Wq", "Ws", "group_off", "ids", "n_groups", "rows", "y", "counts")
 
 
 def grouped_linear(x, W, group_off, *, ids=None, n_groups=None, rows=None, silu=False, y=None,
@@ -594,14 +614,13 @@ def grouped_linear(x, W, group_off, *, ids=None, n_groups=None, rows=None, silu=
     A schedule with B = 1 has them: group_off, uniq, counts[1:2] and task_token.  Returns
     y [M, out] in out_dtype (bf16 or fp32; of the given y, its own); rows in no group are
     left as they were."""
-    D = _linear_dims(("x", "W"), x, W, group_off, ids, n_groups, rows, counts, torch.bfloat16)
-    y, D.out_dtype = _linear_out("y", y, x, D.M, D.out, out_dtype)
-    if silu:
-        D.flags = OMNI_LINEAR_SILU
+    sizes = _linear_sizes(_LINEAR_ARGS, x, W, group_off, ids, n_groups, rows, counts,
+                          torch.bfloat16)
+    y, code = _linear_out("y", y, x, sizes[0], sizes[3], out_dtype)
     index = _index(x)
-    _run("omni_grouped_linear", index, stream, C.byref(D),
-         *_addresses(index, ("x", x), ("W", W), ("group_off", group_off), ("ids", ids),
-                     ("n_groups", n_groups), ("rows", rows), ("y", y), ("counts", counts)))
+    _run("omni_grouped_linear", index, stream,
+         _pack_linear_dims(*sizes, code, OMNI_LINEAR_SILU if silu else 0),
+         *_addresses(index, _LINEAR_ARGS, (x, W, group_off, ids, n_groups, rows, y, counts)))
     return y
 
 
@@ -614,28 +633,29 @@ def grouped_linear_backward(x, W, dy, group_off, *, ids=None, n_groups=None, row
     dW [E, out, in] fp32.  A given dW is added to (accumulate) or overwritten (the matrices of
     no group are left as they were either way); without one, a new dW holds zeros there.
     Returns a dict of those asked for."""
-    D = _linear_dims(("x", "W"), x, W, group_off, ids, n_groups, rows, counts, torch.bfloat16)
-    _expect("dy", dy, D.M * D.out, torch.bfloat16)
+    sizes = _linear_sizes(_BACKWARD_ARGS, x, W, group_off, ids, n_groups, rows, counts,
+                          torch.bfloat16)
+    M, _, n_in, n_out, E, G = sizes
+    _expect("dy", dy, M * n_out, torch.bfloat16)
     if not (need_dx or need_dW):
         raise ValueError("need_dx and need_dW: no gradient asked for")
-    g = {}
+    g, code = {}, OMNI_BF16
     if need_dx:
-        g["dx"], D.out_dtype = _linear_out("dx", dx, x, D.M, D.in_, out_dtype)
+        g["dx"], code = _linear_out("dx", dx, x, M, n_in, out_dtype)
     if need_dW:
         if dW is None:
             # with ids or n_groups some matrices may be in no group
-            make = torch.empty if ids is None and n_groups is None and D.G == D.E \
-                else torch.zeros
-            g["dW"], accumulate = make(W.shape, dtype=torch.float32, device=W.device), False
+            make = torch.empty if ids is None and n_groups is None and G == E else torch.zeros
+            g["dW"] = make(E, n_out, n_in, dtype=torch.float32, device=W.device)
+            accumulate = False
         else:
-            _expect("dW", dW, W.numel(), torch.float32)
+            _expect("dW", dW, E * n_out * n_in, torch.float32)
             g["dW"] = dW
     index = _index(x)
-    _run("omni_grouped_linear_backward", index, stream, C.byref(D),
-         *_addresses(index, ("x", x), ("W", W), ("dy", dy), ("group_off", group_off),
-                     ("ids", ids), ("n_groups", n_groups), ("rows", rows), ("dx", g.get("dx")),
-                     ("dW", g.get("dW"))),
-         1 if accumulate else 0, *_addresses(index, ("counts", counts)))
+    _run("omni_grouped_linear_backward", index, stream, _pack_linear_dims(*sizes, code, 0),
+         *_addresses(index, _BACKWARD_ARGS, (x, W, dy, group_off, ids, n_groups, rows,
+                                             g.get("dx"), g.get("dW"))),
+         1 if accumulate else 0, *_addresses(index, ("counts",), (counts,)))
     return g
 
 
@@ -644,20 +664,26 @@ def quantize_rows(x, *, q=None, scale=None, stream=None):
     scale = max|row| / 127, q = the integer nearest to x / scale (exactly; ties to even).
     x bf16 or f32 [..., width]: tokens [T, in] or weights [E, out, in].  A row with an
     infinity or a NaN gets scale NaN."""
-    code = _out_code("x", x.dtype)
-    if x.dim() < 1:
+    code = _OUT.get(x.dtype)
+    if code is None:
+        raise ValueError(f"x: dtype {x.dtype}, the call reads float32 or bfloat16")
+    shape = x.shape
+    if len(shape) < 1:
         raise ValueError("x: 0 dimensions, the call reads rows")
-    width = x.shape[-1]
+    width = shape[-1]
     n = x.numel() // max(width, 1)
-    _expect("q", q, x.numel(), torch.int8, optional=True)
-    _expect("scale", scale, n, torch.float32, optional=True)
     if q is None:
-        q = x.new_empty(x.shape, dtype=torch.int8)
+        q = torch.empty(*shape, dtype=torch.int8, device=x.device)
+    else:
+        _expect("q", q, x.numel(), torch.int8)
     if scale is None:
-        scale = x.new_empty(x.shape[:-1], dtype=torch.float32)
+        scale = torch.empty(*shape[:-1], dtype=torch.float32, device=x.device) \
+            if len(shape) > 1 else x.new_empty((), dtype=torch.float32)
+    else:
+        _expect("scale", scale, n, torch.float32)
     index = _index(x)
     _run("omni_quantize_rows", index, stream, n, width, code,
-         *_addresses(index, ("x", x), ("q", q), ("scale", scale)))
+         *_addresses(index, ("x", "q", "scale"), (x, q, scale)))
     return q, scale
 
 
@@ -674,17 +700,17 @@ def quantized_linear(xq, xs, Wq, Ws, group_off=None, *, ids=None, n_groups=None,
         if ids is not None or n_groups is not None:
             raise ValueError("group_off is required with ids or n_groups")
         Wq = Wq.unsqueeze(0)
-    D = _linear_dims(("xq", "Wq"), xq, Wq, group_off, ids, n_groups, rows, counts, torch.int8)
-    _expect("xs", xs, D.T, torch.float32)
-    _expect("Ws", Ws, D.E * D.out, torch.float32)
-    y, D.out_dtype = _linear_out("y", y, xq, D.M, D.out, out_dtype)
-    if silu:
-        D.flags = OMNI_LINEAR_SILU
+    sizes = _linear_sizes(("xq", "Wq"), xq, Wq, group_off, ids, n_groups, rows, counts,
+                          torch.int8)
+    M, T, _, n_out, E, _ = sizes
+    _expect("xs", xs, T, torch.float32)
+    _expect("Ws", Ws, E * n_out, torch.float32)
+    y, code = _linear_out("y", y, xq, M, n_out, out_dtype)
     index = _index(xq)
-    _run("omni_quantized_linear", index, stream, C.byref(D),
-         *_addresses(index, ("xq", xq), ("xs", xs), ("Wq", Wq), ("Ws", Ws),
-                     ("group_off", group_off), ("ids", ids), ("n_groups", n_groups),
-                     ("rows", rows), ("y", y), ("counts", counts)))
+    _run("omni_quantized_linear", index, stream,
+         _pack_linear_dims(*sizes, code, OMNI_LINEAR_SILU if silu else 0),
+         *_addresses(index, _QUANTIZED_ARGS, (xq, xs, Wq, Ws, group_off, ids, n_groups, rows, y,
+                                              counts)))
     return y
 
 
