@@ -1040,12 +1040,13 @@ cudaError_t launch(const LinearArgs& a, int sms, cudaStream_t s) {
 // k-block of 128 bytes costs a slot (an SM, or a pair) about
 //   32 wide 305 cycles, 64: 374, 128: 540, pairs of 256: 740;
 // a tile with fewer columns costs in proportion, down to what loading its A
-// and turning a stage over cost.  The estimate is the rounds the slots need for groups of equal size
-// times the mean cost of a tile; the cheapest is taken.  A batch with many
-// rows per group ends up with pairs of 256 (1550 TFLOP/s against 1090 at
-// 128), a decode batch with 32, and a product with few tiles with narrower
-// ones than its rows would fill, so that more SMs have one (300 rows, 2048 to
-// 512: 40 tiles of 32 in 305 cycles a block against 4 pairs in 740).
+// and turning a stage over cost.  The estimate is the rounds the slots need
+// times the cost of the tiles; the cheapest is taken.  A
+// batch with many rows per group ends up with pairs of 256 (1550 TFLOP/s
+// against 1090 at 128), a decode batch with 32, and a product with few tiles
+// with narrower ones than its rows would fill, so that more SMs have one
+// (300 rows, 2048 to 512: 40 tiles of 32 in 305 cycles a block against 4
+// pairs in 740).
 struct Shape {
   int ctas, bn, cycles, least;
 };
@@ -1053,16 +1054,18 @@ constexpr Shape kShapes[] = {
     {1, 32, 305, 305}, {1, 64, 374, 330}, {1, 128, 540, 420}, {2, 256, 740, 480}};
 
 int64_t round_cost(const Shape& sh, int64_t I, int64_t rows, int64_t live, int sms) {
-  const int64_t each = (rows + live - 1) / live;  // rows of a group
-  const int64_t full = each / sh.bn, rest = each % sh.bn;
-  int64_t cost = full * sh.cycles;
-  if (rest > 0) {
-    const int64_t part = sh.cycles * rest / sh.bn;
-    cost += part > sh.least ? part : sh.least;
+  const int64_t each = (rows + live - 1) / live;
+  // the tiles of one group exactly; of many, half a tile more for each group's end
+  int64_t per = live == 1 ? (rows + sh.bn - 1) / sh.bn : (2 * rows / sh.bn + live) / 2;
+  if (per < live) per = live;
+  // groups are uneven: where the mean one fills half a tile, some fill all of it
+  int64_t cost = sh.cycles;
+  if (2 * each < sh.bn) {
+    cost = sh.cycles * each / sh.bn;
+    if (cost < sh.least) cost = sh.least;
   }
-  const int64_t per = full + (rest > 0 ? 1 : 0), slots = sms / sh.ctas;
-  const int64_t tiles = live * per * ((I + kBM * sh.ctas - 1) / (kBM * sh.ctas));
-  return (tiles + slots - 1) / slots * cost / per;
+  const int64_t tiles = per * ((I + kBM * sh.ctas - 1) / (kBM * sh.ctas)), slots = sms / sh.ctas;
+  return (tiles + slots - 1) / slots * cost;
 }
 
 template <Product P, bool F32>
