@@ -484,33 +484,48 @@ __global__ void __launch_bounds__(kThreads, 1)
       // i (the warps' own stores, 64 or 128 bytes each, cost about 10 cycles
       // apiece and bounded short sums); columns cut by a group's end are
       // stored one by one.  dW's columns end with the matrix, where TMA clips.
+      auto stage_chunk = [&](uint32_t buf, const float* z) {
+        const uint32_t to = buf + (32 * quarter + lane) * C::kOutSize;
+#pragma unroll
+        for (int q = 0; q < kOutCols; q += 2) {
+          if constexpr (F32) {
+            asm volatile("st.shared.f32 [%0], %1;" ::"r"(to + q * kBM * 4), "f"(z[q]) : "memory");
+            asm volatile("st.shared.f32 [%0], %1;" ::"r"(to + (q + 1) * kBM * 4), "f"(z[q + 1])
+                         : "memory");
+          } else {
+            const __nv_bfloat162 w = __floats2bfloat162_rn(z[q], z[q + 1]);
+            asm volatile("st.shared.b16 [%0], %1;" ::"r"(to + q * kBM * 2),
+                         "h"(__bfloat16_as_ushort(w.x))
+                         : "memory");
+            asm volatile("st.shared.b16 [%0], %1;" ::"r"(to + (q + 1) * kBM * 2),
+                         "h"(__bfloat16_as_ushort(w.y))
+                         : "memory");
+          }
+        }
+      };
+      auto send_chunk = [&](uint32_t buf, int c) {
+        if constexpr (C::kGradW)
+          store_3d(&maps.out, buf, ic, tl.j0 + c, tl.id, a.accumulate != 0);
+        else
+          store_2d(&maps.out, buf, ic, tl.row0 + tl.j0 + c);
+      };
+      auto next_buf = [&]() -> uint32_t {
+        const uint32_t buf = sOut + out_buf * C::kOutBytes;
+        if (++out_buf == C::kOutBufs) out_buf = 0;
+        return buf;
+      };
       auto leave = [&](int c, const float* z) {
         const int n = tl.n - c;
         if (ic >= I) return;
         if (C::kGradW || n >= kOutCols) {
-          const uint32_t buf = sOut + out_buf * C::kOutBytes;
+          const uint32_t buf = next_buf();
           if (issues)
             asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(C::kOutBufs - 1) : "memory");
           half_sync(half);
-#pragma unroll
-          for (int q = 0; q < kOutCols; ++q) {
-            const uint32_t to = buf + (q * kBM + 32 * quarter + lane) * C::kOutSize;
-            if constexpr (F32)
-              asm volatile("st.shared.f32 [%0], %1;" ::"r"(to), "f"(z[q]) : "memory");
-            else
-              asm volatile("st.shared.b16 [%0], %1;" ::"r"(to),
-                           "h"(__bfloat16_as_ushort(__float2bfloat16_rn(z[q])))
-                           : "memory");
-          }
+          stage_chunk(buf, z);
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           half_sync(half);
-          if (issues) {
-            if constexpr (C::kGradW)
-              store_3d(&maps.out, buf, ic, tl.j0 + c, tl.id, a.accumulate != 0);
-            else
-              store_2d(&maps.out, buf, ic, tl.row0 + tl.j0 + c);
-          }
-          if (++out_buf == C::kOutBufs) out_buf = 0;
+          if (issues) send_chunk(buf, c);
         } else if (i < I) {
           const int64_t at = static_cast<int64_t>(tl.row0 + tl.j0 + c) * I + i;
 #pragma unroll
@@ -524,6 +539,31 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
       };
+      // Two chunks, c and c + 32, for the barriers of one where both are whole:
+      // 16384 x 256 x 4096 in bf16 56 -> 45 us.  Not of fp32, whose stores bound
+      // the way out and then wait for two free buffers (dW of 64 experts, 2048 x
+      // 4096: 441 -> 485 us).
+      auto leave_two = [&](int c, const float* z0, const float* z1) {
+        if (!F32 && C::kOutBufs >= 2 && ic < I && tl.n - c >= 3 * kOutCols) {
+          const uint32_t b0 = next_buf(), b1 = next_buf();
+          if (issues)
+            asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(
+                             C::kOutBufs >= 2 ? C::kOutBufs - 2 : 0)
+                         : "memory");
+          half_sync(half);
+          stage_chunk(b0, z0);
+          stage_chunk(b1, z1);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          half_sync(half);
+          if (issues) {
+            send_chunk(b0, c);
+            send_chunk(b1, c + 2 * kOutCols);
+          }
+        } else {
+          leave(c, z0);
+          leave(c + 2 * kOutCols, z1);
+        }
+      };
       // the scale of column c + lane (lanes 0 .. 15) or c + 16 + lane (16 .. 31)
       auto token_scale = [&](int c) -> float {
         const int j = c + lane + (lane < 16 ? 0 : 16);
@@ -533,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int v = a.rows[r];
         return a.xs[v >= 0 && v < a.T ? v : 0];
       };
-      auto finish = [&](int c, float* z, float xs, int from) {
+      auto finish = [&](float* z, float xs, int from) {
         if constexpr (C::kI8) {
 #pragma unroll
           for (int q = 0; q < kOutCols; ++q)
@@ -544,7 +584,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int q = 0; q < kOutCols; ++q) z[q] = F32 ? silu(z[q]) : silu_fast(z[q]);
         }
-        leave(c, z);
       };
 
       if constexpr (C::kPieces) {
@@ -572,9 +611,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok) break;
 #pragma unroll
-        for (int u = 0; u < kMine; ++u) {
+        for (int u = 0; u < kMine; u += 2) {
           const int c = (2 * u + half) * kOutCols;
-          if (c < tl.n) finish(c, sum[u], 0.0f, 0);
+          if (c >= tl.n) continue;
+          finish(sum[u], 0.0f, 0);
+          if (kMine > 1 && c + 2 * kOutCols < tl.n) {
+            constexpr int kNext = kMine > 1 ? 1 : 0;
+            finish(sum[u + kNext], 0.0f, 0);
+            leave_two(c, sum[u], sum[u + kNext]);
+          } else {
+            leave(c, sum[u]);
+          }
         }
       } else {
         // two chunks at a time
@@ -591,8 +638,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float scale = xs;
           if (c + 4 * kOutCols < tl.n) xs = token_scale(c + 4 * kOutCols);
           else drained();
-          finish(c, reinterpret_cast<float*>(v[0]), scale, 0);
-          if (both) finish(c + 2 * kOutCols, reinterpret_cast<float*>(v[1]), scale, 16);
+          float *z0 = reinterpret_cast<float*>(v[0]), *z1 = reinterpret_cast<float*>(v[1]);
+          finish(z0, scale, 0);
+          if (both) {
+            finish(z1, scale, 16);
+            leave_two(c, z0, z1);
+          } else {
+            leave(c, z0);
+          }
         }
         if (half * kOutCols >= tl.n) drained();
       }
