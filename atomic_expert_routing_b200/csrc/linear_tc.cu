@@ -219,14 +219,19 @@ __device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
                  : "memory");
 }
 
-// SiLU for a bf16 result: the fast exponential and reciprocal are off by at
-// most 2^-17 of the result (the rounding of z / ln 2, |z| < 89), where the
-// rounding to bf16 that follows is off by up to 2^-8.
-__device__ __forceinline__ float silu_fast(float z) {
+// SiLU, z / (1 + e^-z).  For an fp32 result: the exponential is within 2^-23 of
+// its value, the sum within 2^-24, the reciprocal within 2^-23 and the product
+// within 2^-24.  (A division costs 16 columns of a warp about a microsecond.)
+__device__ __forceinline__ float rcp_near(float y) {
   float r;
-  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.0f + __expf(-z)));
-  return z * r;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(y));
+  return r;
 }
+__device__ __forceinline__ float silu_f32(float z) { return z * rcp_near(1.0f + expf(-z)); }
+// For a bf16 result: the fast exponential is off by at most 2^-17 of it (the
+// rounding of z / ln 2, |z| < 89), where the rounding to bf16 that follows is
+// off by up to 2^-8.
+__device__ __forceinline__ float silu_fast(float z) { return z * rcp_near(1.0f + __expf(-z)); }
 
 __device__ __forceinline__ void zero16(uint32_t dst) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst), "r"(0) : "memory");
@@ -333,13 +338,21 @@ struct Cfg {
   static constexpr int kStageA = kSub * kABytes, kStageB = kSub * kBBytes;
   static constexpr int kStage = kStageA + kStageB;
   static constexpr bool kPieces = F32 && !kI8;
+  // Narrow tiles, where a CTA has several: each half of the draining warps takes
+  // every other tile (and so always the same accumulator) whole, since a
+  // tile's fixed costs, not its columns, bound short sums (1 to 4 % of most
+  // small products).  With one tile both halves share it.
+  static constexpr bool kAlternate = BN <= 64 && !kPieces;
   static constexpr int kOutSize = F32 ? 4 : 2, kOutBytes = kOutCols * kBM * kOutSize;
   // chunks each half of the draining warps may have on the way out (dW of
   // 16384 x 2048 x 4096 by 8 experts: 220 us with one, 214 with two, 209 with
   // four; narrow tiles have one chunk per half or two, and stages to keep)
-  static constexpr int kOutBufs = BN >= 128 ? 4 : 1;
+  static constexpr int kOutBufs = BN >= 128 ? 4 : BN == 64 && !F32 ? 2 : 1;
   static constexpr int kOut = 2 * kOutBufs * kOutBytes;
   static constexpr int kCols = 2 * BN;            // TMEM columns
+  static_assert((kSmemLimit - 600 - 1024 - kOut - OMNI_MAX_GROUPS * sizeof(GroupTab)) / kStage >=
+                    kRowWarps,
+                "the row warps' turns need as many stages");
   static_assert(!kGradW || kNb % 64 == 0, "dW's B tile is made of 64-wide boxes");
 };
 
@@ -356,14 +369,18 @@ template <class C, int CTAS, int BN>
 struct TileWalk {
   const LinearArgs& a;
   const GroupTab* tab;
-  int groups, mt, c = 0;
+  int groups, mt;
+  uint32_t inv;  // (2^32 - 1) / mt: a quotient by it is right or one too small
+  int c = 0;
   __device__ __forceinline__ Tile at(int t) {
     while (c + 1 < groups && tab[c + 1].begin <= t) ++c;
     const GroupTab g = tab[c];
     const int local = t - g.begin;
+    int q = static_cast<int>(__umulhi(static_cast<uint32_t>(local), inv));
+    if (local - q * mt >= mt) ++q;
     Tile r;
-    r.i0 = (local % mt) * (kBM * CTAS);
-    r.j0 = (local / mt) * BN;
+    r.i0 = (local - q * mt) * (kBM * CTAS);
+    r.j0 = q * BN;
     const int J = C::kGradW ? a.out : g.rows;
     r.n = J - r.j0 < BN ? J - r.j0 : BN;
     r.row0 = g.row0;
@@ -376,7 +393,7 @@ struct TileWalk {
 template <Product P, int CTAS, int BN, bool F32>
 __global__ void __launch_bounds__(kThreads, 1)
     k_linear_tc(const __grid_constant__ Maps maps, const __grid_constant__ LinearArgs a,
-                int stages) {
+                int stages, int mt, uint32_t mt_inv) {
   using C = Cfg<P, CTAS, BN, F32>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t bars[3 * kMaxStages + 5];
@@ -420,7 +437,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
   const int I = C::kMnA ? a.in : a.out;
-  const int mt = (I + kBM * CTAS - 1) / (kBM * CTAS);
   // dW behind dx: dx lets it start once dx's own wait is over (a.follows), so
   // everything dW reads is there; it waits for dx at its end, before the
   // kernels behind it may start
@@ -444,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const int tiles = scratch.total_tiles;
   const uint32_t tmem = tmem_slot;
-  TileWalk<C, CTAS, BN> walk{a, tab, scratch.total_groups, mt};
+  TileWalk<C, CTAS, BN> walk{a, tab, scratch.total_groups, mt, mt_inv};
   auto n_mma = [](const Tile& t) { return (t.n + 16 * CTAS - 1) / (16 * CTAS) * (16 * CTAS); };
 
   if (warp < kEpiWarps) {
@@ -456,8 +472,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t sOut = sB + stages * C::kStageB + half * C::kOutBufs * C::kOutBytes;
     const bool issues = quarter == 0 && lane == 0;  // this half's stores
     uint32_t acc_no = 0, out_buf = 0;
+    const bool alternate = C::kAlternate && tiles > step;
     bool ok = true;
     for (int t = first; t < tiles && ok; t += step) {
+      if (alternate && static_cast<int>(acc_no & 1) != half) {
+        ++acc_no;
+        continue;
+      }
       const Tile tl = walk.at(t);
       const int ic = tl.i0 + rank * kBM, i = ic + 32 * quarter + lane;
       float ws = 0.0f;
@@ -476,6 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t bar = tempty0 + 8 * (acc_no & 1);
           if (CTAS == 2) arrive_cluster(leader_addr(bar));
           else mbar_arrive(bar);
+          if (alternate) mbar_arrive(bar);  // for the other half's warp
         }
         ++acc_no;
       };
@@ -539,12 +561,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
       };
-      // Two chunks, c and c + 32, for the barriers of one where both are whole:
+      // this warp's chunks: from first_c, gap columns apart
+      const int gap = alternate ? kOutCols : 2 * kOutCols;
+      // Two chunks, gap apart, for the barriers of one where both are whole:
       // 16384 x 256 x 4096 in bf16 56 -> 45 us.  Not of fp32, whose stores bound
       // the way out and then wait for two free buffers (dW of 64 experts, 2048 x
       // 4096: 441 -> 485 us).
       auto leave_two = [&](int c, const float* z0, const float* z1) {
-        if (!F32 && C::kOutBufs >= 2 && ic < I && tl.n - c >= 3 * kOutCols) {
+        if (!F32 && C::kOutBufs >= 2 && ic < I && tl.n - c >= gap + kOutCols) {
           const uint32_t b0 = next_buf(), b1 = next_buf();
           if (issues)
             asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(
@@ -557,16 +581,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           half_sync(half);
           if (issues) {
             send_chunk(b0, c);
-            send_chunk(b1, c + 2 * kOutCols);
+            send_chunk(b1, c + gap);
           }
         } else {
           leave(c, z0);
-          leave(c + 2 * kOutCols, z1);
+          leave(c + gap, z1);
         }
       };
-      // the scale of column c + lane (lanes 0 .. 15) or c + 16 + lane (16 .. 31)
+      const int first_c = alternate ? 0 : half * kOutCols;
+      // the scales of the 16 columns from c (lanes 0 .. 15) and of the next chunk's
       auto token_scale = [&](int c) -> float {
-        const int j = c + lane + (lane < 16 ? 0 : 16);
+        const int j = c + lane + (lane < 16 ? 0 : gap - kOutCols);
         if (!C::kI8 || j >= tl.n) return 0.0f;
         const int r = tl.row0 + tl.j0 + j;
         if (a.rows == nullptr) return a.xs[r];
@@ -582,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!C::kGradW && a.silu) {
 #pragma unroll
-          for (int q = 0; q < kOutCols; ++q) z[q] = F32 ? silu(z[q]) : silu_fast(z[q]);
+          for (int q = 0; q < kOutCols; ++q) z[q] = F32 ? silu_f32(z[q]) : silu_fast(z[q]);
         }
       };
 
@@ -625,18 +650,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       } else {
         // two chunks at a time
-        float xs = token_scale(half * kOutCols);
+        float xs = token_scale(first_c);
         ok = wait_full();
         if (!ok) break;
         const uint32_t acc = tmem + lanes + (acc_no & 1) * BN;
-        for (int c = half * kOutCols; c < tl.n; c += 4 * kOutCols) {
+        for (int c = first_c; c < tl.n; c += 2 * gap) {
           uint32_t v[2][kOutCols];
           tmem_ld16(acc + c, v[0]);
-          const bool both = BN > 2 * kOutCols && c + 2 * kOutCols < tl.n;
-          if (both) tmem_ld16(acc + c + 2 * kOutCols, v[1]);
+          const bool both = gap < BN && c + gap < tl.n;
+          if (both) tmem_ld16(acc + c + gap, v[1]);
           tmem_wait();
           const float scale = xs;
-          if (c + 4 * kOutCols < tl.n) xs = token_scale(c + 4 * kOutCols);
+          if (c + 2 * gap < tl.n) xs = token_scale(c + 2 * gap);
           else drained();
           float *z0 = reinterpret_cast<float*>(v[0]), *z1 = reinterpret_cast<float*>(v[1]);
           finish(z0, scale, 0);
@@ -647,7 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             leave(c, z0);
           }
         }
-        if (half * kOutCols >= tl.n) drained();
+        if (first_c >= tl.n) drained();
       }
     }
     asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // this thread's stores are done
@@ -1052,7 +1077,6 @@ cudaError_t launch(const LinearArgs& a, int sms, cudaStream_t s) {
   const size_t statics = sizeof(GroupScratch) + (3 * kMaxStages + 5) * 8 + 64;
   int stages = static_cast<int>((kSmemLimit - statics - fixed) / C::kStage);
   if (stages > kMaxStages) stages = kMaxStages;
-  if (stages < kRowWarps) return cudaErrorInvalidConfiguration;  // (no case: see wait_empty)
   const size_t smem = fixed + static_cast<size_t>(stages) * C::kStage;
   auto kernel = k_linear_tc<P, CTAS, BN, F32>;
   int dev = 0;
@@ -1085,7 +1109,8 @@ cudaError_t launch(const LinearArgs& a, int sms, cudaStream_t s) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = CTAS == 2 ? 2 : 1;
-  OMNI_TRY(cudaLaunchKernelEx(&cfg, kernel, m, a, stages));
+  OMNI_TRY(cudaLaunchKernelEx(&cfg, kernel, m, a, stages, static_cast<int>(mt),
+                              0xffffffffu / static_cast<uint32_t>(mt)));
   return cudaGetLastError();
 }
 
