@@ -70,6 +70,12 @@ def test_dims_checks(lib, bad, code):
     assert _quantized(lib, D) == code
 
 
+def test_packed_dims_are_the_structure():
+    """The binding packs omni_linear_dims itself."""
+    v = (5, 7, 64, 72, 9, 3, _lib.OMNI_BF16, _lib.OMNI_LINEAR_SILU)
+    assert omni._pack_linear_dims(*v) == bytes(_lib.LinearDims(*v))
+
+
 def test_null_dims(lib):
     assert lib.omni_grouped_linear(None, *([P] * 9)) == BAD
     assert lib.omni_grouped_linear_backward(None, *([P] * 9), 1, P, None) == BAD
