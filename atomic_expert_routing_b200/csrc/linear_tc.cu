@@ -423,9 +423,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   // second tells the first; else the loads of both report to the first.
   const bool halves = gathers;
   if (threadIdx.x == 32 * kLoadWarp) {
-    prefetch_map(&maps.a);
-    if (C::kGradW) prefetch_map(&maps.b);
-    else if (!gathers) prefetch_map(&maps.whole);
+    if (a.g.M > 0) {  // (dW of no rows has no operands)
+      prefetch_map(&maps.a);
+      if (C::kGradW) prefetch_map(&maps.b);
+      else if (!gathers) prefetch_map(&maps.whole);
+    }
     // A stage is full after its loads' two expects.  With gathered rows it is
     // one expect, the threads of one row warp, and in a pair's first CTA the
     // second's word that its half is ready.  Where dW has rows to zero, the
