@@ -13,6 +13,10 @@ Names follow the layer: ``route`` (Cartesian Product Router), ``schedule``
 ``grouped_linear`` and its backward run experts of any width from a schedule
 with one expert per group; ``quantize_rows`` and ``quantized_linear`` are the
 8-bit products.
+
+``stream`` is where a call runs; what it makes itself (outputs, fills) is made
+on that stream too.  Ordering the call's inputs before it, and the use of its
+outputs behind it, is the caller's.
 """
 from __future__ import annotations
 
@@ -83,6 +87,25 @@ def _ptr(t):
 def _stream(stream=None):
     s = torch.cuda.current_stream() if stream is None else stream
     return C.c_void_p(s.cuda_stream)
+
+
+def _new(make, stream, device, dtype, *shape):
+    """A new tensor (make: torch.empty or torch.zeros) of a call on `stream`, made on that stream:
+    its fill is ordered before the call's kernels, and they write no memory that the current
+    stream still uses.  The current stream may use it too, once the caller has ordered the two:
+    its memory is kept for that."""
+    size = shape or ((),)
+    if stream is None:
+        return make(*size, dtype=dtype, device=device)
+    here = torch.cuda.current_stream(device)
+    if stream.cuda_stream == here.cuda_stream:
+        return make(*size, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device)
+    with torch.cuda.stream(stream):
+        t = make(*size, dtype=dtype, device=device)
+    t.record_stream(here)
+    return t
 
 
 def _device(*ts):
@@ -589,12 +612,12 @@ def _run(fn, index, stream, *args):
         _lib.check(fn, code)
 
 
-def _linear_out(name, t, like, M, width, dtype):
+def _linear_out(name, t, like, M, width, dtype, stream):
     """The output [M, width]: t if given (its dtype is the call's), else a new
     tensor of dtype beside like; and its dtype's code."""
     if t is None:
         code = _out_code("out_dtype", dtype)
-        return torch.empty(M, width, dtype=dtype, device=like.device), code
+        return _new(torch.empty, stream, like.device, dtype, M, width), code
     code = _out_code(name, t.dtype)
     _expect(name, t, M * width, t.dtype)
     return t, code
@@ -616,7 +639,7 @@ def grouped_linear(x, W, group_off, *, ids=None, n_groups=None, rows=None, silu=
     left as they were."""
     sizes = _linear_sizes(_LINEAR_ARGS, x, W, group_off, ids, n_groups, rows, counts,
                           torch.bfloat16)
-    y, code = _linear_out("y", y, x, sizes[0], sizes[3], out_dtype)
+    y, code = _linear_out("y", y, x, sizes[0], sizes[3], out_dtype, stream)
     index = _index(x)
     _run("omni_grouped_linear", index, stream,
          _pack_linear_dims(*sizes, code, OMNI_LINEAR_SILU if silu else 0),
@@ -641,12 +664,12 @@ def grouped_linear_backward(x, W, dy, group_off, *, ids=None, n_groups=None, row
         raise ValueError("need_dx and need_dW: no gradient asked for")
     g, code = {}, OMNI_BF16
     if need_dx:
-        g["dx"], code = _linear_out("dx", dx, x, M, n_in, out_dtype)
+        g["dx"], code = _linear_out("dx", dx, x, M, n_in, out_dtype, stream)
     if need_dW:
         if dW is None:
             # with ids or n_groups some matrices may be in no group
             make = torch.empty if ids is None and n_groups is None and G == E else torch.zeros
-            g["dW"] = make(E, n_out, n_in, dtype=torch.float32, device=W.device)
+            g["dW"] = _new(make, stream, W.device, torch.float32, E, n_out, n_in)
             accumulate = False
         else:
             _expect("dW", dW, E * n_out * n_in, torch.float32)
@@ -673,12 +696,11 @@ def quantize_rows(x, *, q=None, scale=None, stream=None):
     width = shape[-1]
     n = x.numel() // max(width, 1)
     if q is None:
-        q = torch.empty(*shape, dtype=torch.int8, device=x.device)
+        q = _new(torch.empty, stream, x.device, torch.int8, *shape)
     else:
         _expect("q", q, x.numel(), torch.int8)
     if scale is None:
-        scale = torch.empty(*shape[:-1], dtype=torch.float32, device=x.device) \
-            if len(shape) > 1 else x.new_empty((), dtype=torch.float32)
+        scale = _new(torch.empty, stream, x.device, torch.float32, *shape[:-1])
     else:
         _expect("scale", scale, n, torch.float32)
     index = _index(x)
@@ -705,7 +727,7 @@ def quantized_linear(xq, xs, Wq, Ws, group_off=None, *, ids=None, n_groups=None,
     M, T, _, n_out, E, _ = sizes
     _expect("xs", xs, T, torch.float32)
     _expect("Ws", Ws, E * n_out, torch.float32)
-    y, code = _linear_out("y", y, xq, M, n_out, out_dtype)
+    y, code = _linear_out("y", y, xq, M, n_out, out_dtype, stream)
     index = _index(xq)
     _run("omni_quantized_linear", index, stream,
          _pack_linear_dims(*sizes, code, OMNI_LINEAR_SILU if silu else 0),
