@@ -89,6 +89,13 @@ def _stream(stream=None):
     return C.c_void_p(s.cuda_stream)
 
 
+def _torch_stream(stream, device):
+    """stream as torch's own type (calls take any object with a cuda_stream)."""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(stream.cuda_stream, device)
+
+
 def _new(make, stream, device, dtype, *shape):
     """A new tensor (make: torch.empty or torch.zeros) of a call on `stream`, made on that stream:
     its fill is ordered before the call's kernels, and they write no memory that the current
@@ -100,9 +107,7 @@ def _new(make, stream, device, dtype, *shape):
     here = torch.cuda.current_stream(device)
     if stream.cuda_stream == here.cuda_stream:
         return make(*size, dtype=dtype, device=device)
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(stream.cuda_stream, device)
-    with torch.cuda.stream(stream):
+    with torch.cuda.stream(_torch_stream(stream, device)):
         t = make(*size, dtype=dtype, device=device)
     t.record_stream(here)
     return t
@@ -176,26 +181,40 @@ class Workspace:
 
     def __init__(self):
         self.buf = None
+        self._users = set()  # the streams that its memory is kept for
 
-    def get(self, nbytes: int, device) -> torch.Tensor | None:
+    def get(self, nbytes: int, device, stream=None) -> torch.Tensor | None:
+        """A buffer of nbytes for a call on stream (default: the current one)."""
         if nbytes == 0:
             return None
         if self.buf is None or self.buf.numel() < nbytes or self.buf.device != device:
-            self.buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
+            self.buf = _new(torch.empty, stream, device, torch.uint8, nbytes)
+            self._users = set()
+        if self.buf.device.type == "cpu":
+            return self.buf  # refused by the call
+        on = torch.cuda.current_stream(device) if stream is None else stream
+        if on.cuda_stream not in self._users:
+            # it may be another stream's memory, and be let go while this call runs
+            self.buf.record_stream(_torch_stream(on, device))
+            self._users.add(on.cuda_stream)
         return self.buf
 
 
-def _ws(D, which, device, ws):
+def _ws(D, which, device, ws, stream):
     n = workspace_size(D, which)
     if ws is None:
         ws = Workspace()
-    buf = ws.get(n, device)
+    buf = ws.get(n, device, stream)
     return (_ptr(buf) if buf is not None else None), n
 
 
 def new_counts(device) -> torch.Tensor:
     """Zeroed int32[4] device counters: n_active, n_groups, status bits, reserved."""
     return torch.zeros(4, dtype=torch.int32, device=device)
+
+
+def _new_counts(device, stream):
+    return _new(torch.zeros, stream, device, torch.int32, 4)
 
 
 def route(D: LayerDims, x, Wr, Wc, bias_r=None, bias_c=None, *, counts=None, ws=None,
@@ -208,10 +227,10 @@ def route(D: LayerDims, x, Wr, Wc, bias_r=None, bias_c=None, *, counts=None, ws=
         idx, gate = out
         _expect_io(D, idx=idx, gate=gate)
     else:
-        idx = torch.empty((D.L, D.K), dtype=torch.int32, device=dev)
-        gate = torch.empty((D.L, D.K), dtype=torch.float32, device=dev)
-    score = torch.empty((D.L, D.K), dtype=torch.float32, device=dev) if with_score else None
-    wsp, n = _ws(D, OMNI_WS_ROUTE, dev, ws)
+        idx = _new(torch.empty, stream, dev, torch.int32, D.L, D.K)
+        gate = _new(torch.empty, stream, dev, torch.float32, D.L, D.K)
+    score = _new(torch.empty, stream, dev, torch.float32, D.L, D.K) if with_score else None
+    wsp, n = _ws(D, OMNI_WS_ROUTE, dev, ws, stream)
     dd = D.c()
     _lib.check("omni_route", _lib.load().omni_route(
         C.byref(dd), _ptr(x), _ptr(Wr), _ptr(Wc), _ptr(bias_r), _ptr(bias_c), _ptr(idx),
@@ -223,8 +242,8 @@ def router_logits(D: LayerDims, x, Wr, Wc, *, counts=None, ws=None, stream=None)
     """Router projections: float32 [L, Nr + Nc] (row logits, then column logits)."""
     _expect_io(D, x=x, Wr=Wr, Wc=Wc, counts=counts)
     dev = _device(x)
-    z = torch.empty((D.L, D.Nr + D.Nc), dtype=torch.float32, device=dev)
-    wsp, n = _ws(D, OMNI_WS_ROUTE, dev, ws)
+    z = _new(torch.empty, stream, dev, torch.float32, D.L, D.Nr + D.Nc)
+    wsp, n = _ws(D, OMNI_WS_ROUTE, dev, ws, stream)
     dd = D.c()
     _lib.check("omni_router_logits", _lib.load().omni_router_logits(
         C.byref(dd), _ptr(x), _ptr(Wr), _ptr(Wc), _ptr(z), _ptr(counts), wsp, n,
@@ -236,9 +255,9 @@ def route_select(D: LayerDims, logits, bias_r=None, bias_c=None, *, counts=None,
     """Selection from axis logits [L, Nr + Nc] (float32)."""
     _expect_io(D, logits=logits, bias_r=bias_r, bias_c=bias_c, counts=counts)
     dev = _device(logits)
-    idx = torch.empty((D.L, D.K), dtype=torch.int32, device=dev)
-    gate = torch.empty((D.L, D.K), dtype=torch.float32, device=dev)
-    score = torch.empty((D.L, D.K), dtype=torch.float32, device=dev)
+    idx = _new(torch.empty, stream, dev, torch.int32, D.L, D.K)
+    gate = _new(torch.empty, stream, dev, torch.float32, D.L, D.K)
+    score = _new(torch.empty, stream, dev, torch.float32, D.L, D.K)
     dd = D.c()
     _lib.check("omni_route_select", _lib.load().omni_route_select(
         C.byref(dd), _ptr(logits), _ptr(bias_r), _ptr(bias_c), _ptr(idx), _ptr(gate),
@@ -256,14 +275,14 @@ def schedule(D: LayerDims, idx, gate, *, counts=None, ws=None, stream=None) -> d
     ucap = max(1, min(D.N, M))
     gmax = (ucap + D.B - 1) // D.B
     out = {
-        "task_token": torch.empty(M, dtype=torch.int32, device=dev),
-        "task_expert": torch.empty(M, dtype=torch.int32, device=dev),
-        "task_gate": torch.empty(M, dtype=torch.float32, device=dev),
-        "uniq": torch.empty(ucap, dtype=torch.int32, device=dev),
-        "group_off": torch.empty(gmax + 1, dtype=torch.int32, device=dev),
-        "counts": new_counts(dev) if counts is None else counts,
+        "task_token": _new(torch.empty, stream, dev, torch.int32, M),
+        "task_expert": _new(torch.empty, stream, dev, torch.int32, M),
+        "task_gate": _new(torch.empty, stream, dev, torch.float32, M),
+        "uniq": _new(torch.empty, stream, dev, torch.int32, ucap),
+        "group_off": _new(torch.empty, stream, dev, torch.int32, gmax + 1),
+        "counts": _new_counts(dev, stream) if counts is None else counts,
     }
-    wsp, n = _ws(D, OMNI_WS_SCHEDULE, dev, ws)
+    wsp, n = _ws(D, OMNI_WS_SCHEDULE, dev, ws, stream)
     dd = D.c()
     _lib.check("omni_schedule", _lib.load().omni_schedule(
         C.byref(dd), _ptr(idx), _ptr(gate), _ptr(out["task_token"]), _ptr(out["task_expert"]),
@@ -288,8 +307,8 @@ def expert_forward(D: LayerDims, x, W, V, sched: dict, *, U=None, y=None, ws=Non
     _expect_sched(D, sched)
     dev = _device(x)
     if y is None:
-        y = torch.empty((D.L, D.d), dtype=D.torch_dtype, device=dev)
-    wsp, n = _ws(D, OMNI_WS_EXPERT, dev, ws)
+        y = _new(torch.empty, stream, dev, D.torch_dtype, D.L, D.d)
+    wsp, n = _ws(D, OMNI_WS_EXPERT, dev, ws, stream)
     dd = D.c()
     fn, wts = _weights("omni_expert_forward", W, U, V)
     _lib.check(fn, getattr(_lib.load(), fn)(
@@ -308,7 +327,7 @@ def expert_forward_noalloc(D: LayerDims, x, W, V, sched: dict, *, y=None, stream
     _expect_sched(D, sched)
     dev = _device(x)
     if y is None:
-        y = torch.empty((D.L, D.d), dtype=D.torch_dtype, device=dev)
+        y = _new(torch.empty, stream, dev, D.torch_dtype, D.L, D.d)
     dd = D.c()
     args = (_ptr(x), _ptr(W), _ptr(V), _ptr(sched["task_token"]), _ptr(sched["task_expert"]),
             _ptr(sched["task_gate"]), _ptr(sched["uniq"]), _ptr(sched["group_off"]),
@@ -328,10 +347,10 @@ def moe_forward(D: LayerDims, x, Wr, Wc, W, V, bias_r=None, bias_c=None, *, U=No
                counts=counts, idx=idx, gate=gate)
     dev = _device(x)
     if y is None:
-        y = torch.empty((D.L, D.d), dtype=D.torch_dtype, device=dev)
+        y = _new(torch.empty, stream, dev, D.torch_dtype, D.L, D.d)
     if counts is None:
-        counts = new_counts(dev)
-    wsp, n = _ws(D, OMNI_WS_FUSED, dev, ws)
+        counts = _new_counts(dev, stream)
+    wsp, n = _ws(D, OMNI_WS_FUSED, dev, ws, stream)
     dd = D.c()
     fn, wts = _weights("omni_moe_forward", W, U, V)
     _lib.check(fn, getattr(_lib.load(), fn)(
@@ -358,10 +377,10 @@ def moe_forward_shard(D: LayerDims, x, Wr, Wc, W, V, e_lo: int, e_hi: int, bias_
     _expect("y_part", y_part, D.L * D.d, torch.float32, optional=True)
     dev = _device(x)
     if y_part is None:
-        y_part = torch.empty((D.L, D.d), dtype=torch.float32, device=dev)
+        y_part = _new(torch.empty, stream, dev, torch.float32, D.L, D.d)
     if counts is None:
-        counts = new_counts(dev)
-    wsp, n = _ws(D, OMNI_WS_FUSED, dev, ws)
+        counts = _new_counts(dev, stream)
+    wsp, n = _ws(D, OMNI_WS_FUSED, dev, ws, stream)
     dd = D.c()
     _lib.check("omni_moe_forward_shard", _lib.load().omni_moe_forward_shard(
         C.byref(dd), e_lo, e_hi, _ptr(x), _ptr(Wr), _ptr(Wc), _ptr(bias_r), _ptr(bias_c),
@@ -385,10 +404,10 @@ def moe_forward_shard_routed(D: LayerDims, x, W, V, e_lo: int, e_hi: int, idx, g
     _expect("y_part", y_part, D.L * D.d, torch.float32, optional=True)
     dev = _device(x)
     if y_part is None:
-        y_part = torch.empty((D.L, D.d), dtype=torch.float32, device=dev)
+        y_part = _new(torch.empty, stream, dev, torch.float32, D.L, D.d)
     if counts is None:
-        counts = new_counts(dev)
-    wsp, n = _ws(D, OMNI_WS_FUSED, dev, ws)
+        counts = _new_counts(dev, stream)
+    wsp, n = _ws(D, OMNI_WS_FUSED, dev, ws, stream)
     dd = D.c()
     _lib.check("omni_moe_forward_shard_routed", _lib.load().omni_moe_forward_shard_routed(
         C.byref(dd), e_lo, e_hi, _ptr(x), _ptr(W), _ptr(U), _ptr(V), _ptr(idx), _ptr(gate),
@@ -401,7 +420,7 @@ def cast_output(D: LayerDims, src, *, y=None, stream=None):
     _expect("src", src, D.L * D.d, torch.float32)
     _expect_io(D, y=y)
     if y is None:
-        y = torch.empty((D.L, D.d), dtype=D.torch_dtype, device=_device(src))
+        y = _new(torch.empty, stream, _device(src), D.torch_dtype, D.L, D.d)
     dd = D.c()
     _lib.check("omni_cast_output", _lib.load().omni_cast_output(
         C.byref(dd), _ptr(src), _ptr(y), _stream(stream)))
@@ -429,14 +448,14 @@ def moe_backward(D: LayerDims, x, Wr, Wc, W, V, idx, gate, dy, *, grads=None, bi
             g.pop(name, None)
             continue
         if name not in g:
-            g[name] = (torch.empty if name == "dx" else torch.zeros)(shape, dtype=f32, device=dev)
+            g[name] = _new(torch.empty if name == "dx" else torch.zeros, stream, dev, f32, *shape)
         n = 1
         for v in shape:
             n *= v
         _expect(name, g[name], n, f32)
     if counts is None:
-        counts = new_counts(dev)
-    wsp, n = _ws(D, OMNI_WS_BACKWARD, dev, ws)
+        counts = _new_counts(dev, stream)
+    wsp, n = _ws(D, OMNI_WS_BACKWARD, dev, ws, stream)
     dd = D.c()
     _lib.check("omni_moe_backward", _lib.load().omni_moe_backward(
         C.byref(dd), _ptr(x), _ptr(Wr), _ptr(Wc), _ptr(W), _ptr(V), _ptr(idx), _ptr(gate),
@@ -469,9 +488,9 @@ def shared_mlp(D: LayerDims, x, W1, W2, *, y=None, accumulate=False, counts=None
         raise ValueError("y is required to accumulate into")
     dev = _device(x)
     if y is None:
-        y = torch.empty((D.L, D.d), dtype=D.torch_dtype, device=dev)
+        y = _new(torch.empty, stream, dev, D.torch_dtype, D.L, D.d)
     n = mlp_workspace_size(D, F, False)
-    buf = (Workspace() if ws is None else ws).get(n, dev)
+    buf = (Workspace() if ws is None else ws).get(n, dev, stream)
     dd = D.c()
     _lib.check("omni_shared_mlp", _lib.load().omni_shared_mlp(
         C.byref(dd), C.c_int64(F), _ptr(x), _ptr(W1), _ptr(W2), _ptr(y), 1 if accumulate else 0,
@@ -488,11 +507,11 @@ def moe_mlp_forward(D: LayerDims, x, Wr, Wc, W, V, W1, W2, bias_r=None, bias_c=N
     _expect_mlp(D, F, W1, W2)
     dev = _device(x)
     if y is None:
-        y = torch.empty((D.L, D.d), dtype=D.torch_dtype, device=dev)
+        y = _new(torch.empty, stream, dev, D.torch_dtype, D.L, D.d)
     if counts is None:
-        counts = new_counts(dev)
+        counts = _new_counts(dev, stream)
     n = mlp_workspace_size(D, F, True)
-    buf = (Workspace() if ws is None else ws).get(n, dev)
+    buf = (Workspace() if ws is None else ws).get(n, dev, stream)
     dd = D.c()
     _lib.check("omni_moe_mlp_forward", _lib.load().omni_moe_mlp_forward(
         C.byref(dd), C.c_int64(F), _ptr(x), _ptr(Wr), _ptr(Wc), _ptr(bias_r), _ptr(bias_c),
@@ -510,7 +529,7 @@ def token_centric_forward(D: LayerDims, x, W, V, idx, gate, *, U=None, y=None, c
     _expect("gate", gate, D.M, torch.float32)
     dev = _device(x)
     if y is None:
-        y = torch.empty((D.L, D.d), dtype=D.torch_dtype, device=dev)
+        y = _new(torch.empty, stream, dev, D.torch_dtype, D.L, D.d)
     dd = D.c()
     fn, wts = _weights("omni_token_centric_forward", W, U, V)
     _lib.check(fn, getattr(_lib.load(), fn)(

@@ -86,3 +86,42 @@ def test_outputs_in_use_by_the_current_stream_are_kept(name):
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(copies, ref))
     assert not any(bool(t.float().any()) for t in later)
+
+
+def _layer():
+    g = torch.Generator(device="cuda")
+    g.manual_seed(61)
+
+    def normal(*shape, std=1.0):
+        return (torch.randn(shape, generator=g, device="cuda") * std).to(BF)
+
+    D = omni.LayerDims(L=64, d=256, Nr=8, Nc=8, k=4, K=4, B=1)
+    return D, dict(x=normal(64, 256), Wr=normal(8, 256, std=0.06), Wc=normal(8, 256, std=0.06),
+                   W=normal(64, 256, std=0.06), V=normal(64, 256), dy=normal(64, 256))
+
+
+def test_schedule_and_backward_behind_a_busy_stream():
+    """The counters and the parameter gradients that a call zeroes itself.  The counts are exact;
+    the gradients are compared with the same call on the current stream."""
+    D, p = _layer()
+    rt = (p["x"], p["Wr"], p["Wc"], p["W"], p["V"])
+    idx, gate, _ = omni.route(D, *rt[:3])
+    s0 = omni.schedule(D, idx, gate)
+    g0 = omni.moe_backward(D, *rt, idx, gate, p["dy"])
+    other = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(LONG)
+    s1 = omni.schedule(D, idx, gate, stream=other)
+    g1 = omni.moe_backward(D, *rt, idx, gate, p["dy"], stream=other)
+    other.synchronize()
+    torch.cuda.synchronize()
+    n, groups = (int(v) for v in s0["counts"][:2])
+    assert torch.equal(s0["counts"], s1["counts"]) and n > 0
+    for k, m in (("task_token", D.M), ("task_expert", D.M), ("uniq", n), ("group_off", groups + 1)):
+        assert torch.equal(s0[k][:m], s1[k][:m])
+    for k, a in g0.items():
+        # atomics add in any order (2^-23 a term, 256 terms), and a term that is rounded to bf16
+        # next may then fall on the other side of a border (two half steps, 2^-7 of it); a term
+        # is taken as up to twice the largest result
+        tol = 2 * (2.0 ** -7 + 256 * 2.0 ** -23) * float(a.abs().max())
+        assert bool(a.any()) and float((a - g1[k]).abs().max()) <= tol
