@@ -277,7 +277,7 @@ cudaError_t launch_bn(const Dims& D, const CUtensorMap& a, const CUtensorMap& br
 // K-splits from the dims alone (so workspace sizes are known on the host):
 // enough CTAs for about one per SM of a 148-SM B200, at most 16 partials.
 int router_splits(const Dims& D) {
-  if (D.dtype != OMNI_BF16 || (D.flags & OMNI_FLAG_ROUTER_SIMT)) return 1;
+  if (D.dtype != OMNI_BF16 || (D.flags & OMNI_FLAG_ROUTER_SIMT) || D.L == 0) return 1;
   const int bn = pick_bn(D);
   const int64_t tiles = ((D.L + TC_BM - 1) / TC_BM) *
                         ((D.Nr + bn - 1) / bn + (D.Nc + bn - 1) / bn);
