@@ -39,6 +39,7 @@
 #include <atomic>
 
 #include "linear.cuh"
+#include "linear_plan.h"
 #include "tc_common.cuh"
 
 namespace omni {
@@ -871,6 +872,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       if constexpr (C::kGradW) {
         uint32_t tails = 0;
+        WaitSpan span;
         for (int t = first; t < tiles && ok; t += step) {
           const Tile tl = walk.at(t);
           const int blocks = (tl.K + 63) / 64, last = tl.K - 64 * (blocks - 1);
@@ -878,13 +880,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int tail_s = static_cast<int>((no + blocks - 1) % stages);
           // zeroes the rows past the group's end up to the last product's 16, of
           // both operands: what is there may be infinite
+          span.tile(blocks);
           auto zero_tail = [&]() {
-            // (without gathered rows the whole group is summed during this wait:
-            // a quarter of a million blocks take a tenth of a second)
+            // (with gathered rows this warp has just taken the same stage)
             ok = __all_sync(0xffffffffu,
                             wait_for<false>(tail0 + 8 * tail_s, (tails >> tail_s) & 1, a.status,
-                                            1 + (static_cast<uint32_t>(blocks) >> 18)));
+                                            gathers ? 1 : span.limits()));
             if (!ok) return;
+            span.waited();
             const uint32_t da = sA + tail_s * C::kStageA, db = sB + tail_s * C::kStageB;
             const int chunks = (n_mma(tl) / CTAS + 63) / 64;
             for (int g = lane; g < (16 - (last & 15)) * 8; g += 32) {
