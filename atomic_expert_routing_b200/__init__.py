@@ -563,14 +563,19 @@ def _misplaced(name, t, index):
     raise ValueError("tensors passed to the CUDA library must be contiguous")
 
 
+_NO_ELEMENTS = 1 << 12  # what stands for the address of a tensor without elements
+
+
 def _addresses(index, names, tensors):
-    """The addresses of tensors (None: no tensor), contiguous on CUDA device `index`."""
+    """The addresses of tensors (None: no tensor), contiguous on CUDA device `index`.  A tensor
+    without elements has none of its own: it gets one that is not NULL, which the library takes
+    as no tensor, and which is never read."""
     out = []
     for t in tensors:
         if t is None:
             out.append(None)
         elif t.get_device() == index and t.is_contiguous():
-            out.append(t.data_ptr())
+            out.append(t.data_ptr() or _NO_ELEMENTS)
         else:
             _misplaced(names[len(out)], t, index)
     return out

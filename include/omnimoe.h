@@ -453,6 +453,9 @@ typedef struct omni_linear_dims {
  * an id outside [0, E) or not above every earlier id, or a group count
  * outside [0, G] (clamped) sets OMNI_DEV_BAD_INDEX, and the group is left
  * out (without ids its dW is that of a group without rows); so does an entry of rows outside [0, T), which is taken as row 0.
+ * With M == 0 no array of product rows (rows, dy, y, dx) is read or written;
+ * a NULL keeps its meaning (no row list, no gradient), so pass any other
+ * address for an array that is there without elements.
  * The calls need no workspace.  Outputs must not overlap any input. */
 
 /*
