@@ -588,6 +588,25 @@ def _index(t):
     return t.get_device()
 
 
+def _expect_rows(name, t, n, width, dtype):
+    """_expect, of n rows of the given width (a tuple, innermost last).  A tensor of one dimension
+    is memory that the caller shapes; of one with more the rows have that width: the count of
+    elements does not tell a transposed one."""
+    each = 1
+    for w in width:
+        each *= w
+    _expect(name, t, n * each, dtype)
+    shape = t.shape
+    if len(shape) < 2 or n == 0 or shape[-1] == each:
+        return
+    held = [v for v in shape if v != 1]  # a dimension of one element lays nothing out
+    if len(held) < 2 or held[-1] == each or held[-1] == width[-1] and (
+            len(held) < 3 or held[-2] == width[-2]):
+        return
+    raise ValueError(f"{name}: shape {tuple(shape)}, the call takes {n} rows of "
+                     f"{' x '.join(map(str, width))}")
+
+
 def _linear_sizes(names, x, W, group_off, ids, n_groups, rows, counts, dtype):
     """The checks the grouped products share, and the sizes (M, T, in, out, E, G) of a call of
     x [T, in] with W [E, out, in] of the given dtype."""
@@ -643,7 +662,7 @@ def _linear_out(name, t, like, M, width, dtype, stream):
         code = _out_code("out_dtype", dtype)
         return _new(torch.empty, stream, like.device, dtype, M, width), code
     code = _out_code(name, t.dtype)
-    _expect(name, t, M * width, t.dtype)
+    _expect_rows(name, t, M, (width,), t.dtype)
     return t, code
 
 
@@ -675,15 +694,15 @@ def grouped_linear_backward(x, W, dy, group_off, *, ids=None, n_groups=None, row
                             dx=None, dW=None, need_dx=True, need_dW=True,
                             out_dtype=torch.bfloat16, accumulate=True, counts=None,
                             stream=None):
-    """Gradients of the loss sum(dy * y) of grouped_linear (without silu): dx [M, in], one row
-    per product row (out_dtype, overwritten; with rows, add up the rows of a token), and
-    dW [E, out, in] fp32.  A given dW is added to (accumulate) or overwritten (the matrices of
-    no group are left as they were either way); without one, a new dW holds zeros there.
-    Returns a dict of those asked for."""
+    """Gradients of the loss sum(dy * y) of grouped_linear (without silu), dy [M, out] bf16:
+    dx [M, in], one row per product row (out_dtype, overwritten; with rows, add up the rows of a
+    token), and dW [E, out, in] fp32.  A given dW is added to (accumulate) or overwritten (the
+    matrices of no group are left as they were either way); without one, a new dW holds zeros
+    there.  Returns a dict of those asked for."""
     sizes = _linear_sizes(_BACKWARD_ARGS, x, W, group_off, ids, n_groups, rows, counts,
                           torch.bfloat16)
     M, _, n_in, n_out, E, G = sizes
-    _expect("dy", dy, M * n_out, torch.bfloat16)
+    _expect_rows("dy", dy, M, (n_out,), torch.bfloat16)
     if not (need_dx or need_dW):
         raise ValueError("need_dx and need_dW: no gradient asked for")
     g, code = {}, OMNI_BF16
@@ -696,7 +715,7 @@ def grouped_linear_backward(x, W, dy, group_off, *, ids=None, n_groups=None, row
             g["dW"] = _new(make, stream, W.device, torch.float32, E, n_out, n_in)
             accumulate = False
         else:
-            _expect("dW", dW, E * n_out * n_in, torch.float32)
+            _expect_rows("dW", dW, E, (n_out, n_in), torch.float32)
             g["dW"] = dW
     index = _index(x)
     _run("omni_grouped_linear_backward", index, stream, _pack_linear_dims(*sizes, code, 0),
@@ -722,7 +741,7 @@ def quantize_rows(x, *, q=None, scale=None, stream=None):
     if q is None:
         q = _new(torch.empty, stream, x.device, torch.int8, *shape)
     else:
-        _expect("q", q, x.numel(), torch.int8)
+        _expect_rows("q", q, n, (width,), torch.int8)
     if scale is None:
         scale = _new(torch.empty, stream, x.device, torch.float32, *shape[:-1])
     else:
@@ -750,7 +769,7 @@ def quantized_linear(xq, xs, Wq, Ws, group_off=None, *, ids=None, n_groups=None,
                           torch.int8)
     M, T, _, n_out, E, _ = sizes
     _expect("xs", xs, T, torch.float32)
-    _expect("Ws", Ws, E * n_out, torch.float32)
+    _expect_rows("Ws", Ws, E, (n_out,), torch.float32)
     y, code = _linear_out("y", y, xq, M, n_out, out_dtype, stream)
     index = _index(xq)
     _run("omni_quantized_linear", index, stream,
