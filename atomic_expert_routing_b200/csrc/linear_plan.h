@@ -25,4 +25,27 @@ struct WaitSpan {
   OMNI_HOST_DEVICE void waited() { blocks = 0; }
 };
 
+// Results leave through shared memory in chunks of 16 columns of 128.
+constexpr int kOutCols = 16;
+
+// How a warp's chunks of a tile of n columns leave.  They lie gap columns
+// apart and go two at a time; those that go through shared memory take the
+// barrier of the four warps of a half twice.
+struct DrainRule {
+  bool clipped;  // columns end with the matrix, not with a group: TMA cuts them
+  bool pairs;    // two whole chunks may share the barriers of one
+  int gap;
+  OMNI_HOST_DEVICE bool whole(int left) const { return clipped || left >= kOutCols; }
+  OMNI_HOST_DEVICE bool two(int left) const { return pairs && left >= gap + kOutCols; }
+  // the barriers of a tile, for a warp whose first chunk is at column c
+  OMNI_HOST_DEVICE int barriers(int n, int c) const {
+    int b = 0;
+    for (; c < n; c += 2 * gap) {
+      if (two(n - c)) b += 2;
+      else b += 2 * (whole(n - c) ? 1 : 0) + 2 * (c + gap < n && whole(n - c - gap) ? 1 : 0);
+    }
+    return b;
+  }
+};
+
 }  // namespace omni

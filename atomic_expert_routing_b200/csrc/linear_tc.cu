@@ -59,8 +59,6 @@ constexpr int kThreads = 32 * (kEpiWarps + 4 + kRowWarps);
 // (128 sums a thread) go to 184, the other two to 72: 2 * 184 + 2 * 72 = 4 * 128.
 constexpr int kLaunchRegs = 128, kEpiRegs = 184, kOtherRegs = 72;
 static_assert(2 * kEpiRegs + 2 * kOtherRegs == 4 * kLaunchRegs && kThreads == 512, "");
-// Results leave through shared memory in chunks of 16 columns of 128
-constexpr int kOutCols = 16;
 constexpr int kPiece = 512;         // terms of k in a piece
 constexpr size_t kSmemLimit = 227 * 1024;
 
@@ -484,8 +482,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool issues = quarter == 0 && lane == 0;  // this half's stores
     uint32_t acc_no = 0, out_buf = 0;
     const bool alternate = C::kAlternate && tiles > step;
+    // this warp's chunks of columns: from first_c, gap columns apart
+    const int gap = alternate ? kOutCols : 2 * kOutCols, first_c = alternate ? 0 : half * kOutCols;
+    const DrainRule rule{C::kGradW, !F32 && C::kOutBufs >= 2, gap};
     bool ok = true;
-    for (int t = first; t < tiles && ok; t += step) {
+    int t = first;
+    for (; t < tiles; t += step) {
       if (alternate && static_cast<int>(acc_no & 1) != half) {
         ++acc_no;
         continue;
@@ -550,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto leave = [&](int c, const float* z) {
         const int n = tl.n - c;
         if (ic >= I) return;
-        if (C::kGradW || n >= kOutCols) {
+        if (rule.whole(n)) {
           const uint32_t buf = next_buf();
           if (issues)
             asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(C::kOutBufs - 1) : "memory");
@@ -572,14 +574,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
       };
-      // this warp's chunks: from first_c, gap columns apart
-      const int gap = alternate ? kOutCols : 2 * kOutCols;
       // Two chunks, gap apart, for the barriers of one where both are whole:
       // 16384 x 256 x 4096 in bf16 56 -> 45 us.  Not of fp32, whose stores bound
       // the way out and then wait for two free buffers (dW of 64 experts, 2048 x
       // 4096: 441 -> 485 us).
       auto leave_two = [&](int c, const float* z0, const float* z1) {
-        if (!F32 && C::kOutBufs >= 2 && ic < I && tl.n - c >= gap + kOutCols) {
+        if (ic < I && rule.two(tl.n - c)) {
           const uint32_t b0 = next_buf(), b1 = next_buf();
           if (issues)
             asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(
@@ -599,7 +599,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           leave(c + gap, z1);
         }
       };
-      const int first_c = alternate ? 0 : half * kOutCols;
       // the scales of the 16 columns from c (lanes 0 .. 15) and of the next chunk's
       auto token_scale = [&](int c) -> float {
         const int j = c + lane + (lane < 16 ? 0 : gap - kOutCols);
@@ -686,6 +685,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (first_c >= tl.n) drained();
       }
     }
+    // A wait ran out.  The half's barriers have no limit and take all four
+    // warps, whose waits need not run out alike: this warp still comes to the
+    // barriers of the tile that it was waiting for and of all behind it.  It
+    // frees no accumulator any more, so the products stop and the other warps'
+    // waits run out in turn.
+    if (!ok)
+      for (; t < tiles; t += step) {
+        if (alternate && static_cast<int>(acc_no++ & 1) != half) continue;
+        const Tile tl = walk.at(t);
+        if (tl.i0 + rank * kBM >= I) continue;
+        for (int q = rule.barriers(tl.n, first_c); q > 0; --q) half_sync(half);
+      }
     asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // this thread's stores are done
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
