@@ -32,6 +32,11 @@ struct GroupScratch {
   int32_t total_tiles, total_groups;
 };
 
+// An entry of a caller's array, read from L2.  dW behind dx of the same call
+// may start before it has waited for the kernels ahead itself (LinearArgs), and
+// so reads nothing through L1, which might hold what was there before them.
+__device__ __forceinline__ int32_t fresh(const int32_t* p) { return __ldcg(p); }
+
 // Builds the table of the groups that have tiles, in order, with the CTA's
 // first kGroupWarps warps (the caller's barrier makes it visible).
 // tiles_of(rows): tiles of a group of that many rows, 0 to leave it out.  A
@@ -62,13 +67,13 @@ __device__ __forceinline__ void build_groups(const Groups& P, const TilesOf& til
   int32_t a = 0, b = 0, id = -1;
   auto load = [&](int g) {  // G entries exist whatever the count says
     const bool there = g < P.G;
-    a = there ? P.off[g] : 0;
-    b = there ? P.off[g + 1] : 0;
-    id = !there ? -1 : P.ids != nullptr ? P.ids[g] : g;
+    a = there ? fresh(P.off + g) : 0;
+    b = there ? fresh(P.off + g + 1) : 0;
+    id = !there ? -1 : P.ids != nullptr ? fresh(P.ids + g) : g;
   };
   load(tid);
   if (P.n_groups != nullptr) {
-    const int v = *P.n_groups;
+    const int v = fresh(P.n_groups);
     bad = v < 0 || v > n;
     n = v < 0 ? 0 : (v > n ? n : v);
   }
@@ -165,7 +170,13 @@ struct LinearArgs {
   int64_t T;
   int32_t in, out;
   int32_t out_f32, silu, accumulate;
-  int32_t leads, follows;  // dx and dW of one call, which may run side by side
+  // dx (leads) and dW (follows) of one call may run side by side: dx lets dW
+  // start once its own wait for the kernels ahead is over.  Their writes are
+  // complete by then, in the L2; that a kernel which has not waited itself sees
+  // them there is an assumption beyond what the programming model states for
+  // dependent launches, so dW reads x, dy, rows and the group arrays from L2
+  // only (TMA, cp.async.cg, fresh()).
+  int32_t leads, follows;
   const int32_t* rows;  // nullable
   const void* x;        // [T x in]
   const void* W;        // [E x out x in]

@@ -446,9 +446,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
   const int I = C::kMnA ? a.in : a.out;
-  // dW behind dx: dx lets it start once dx's own wait is over (a.follows), so
-  // everything dW reads is there; it waits for dx at its end, before the
-  // kernels behind it may start
+  // dW behind dx (LinearArgs::follows) starts without a wait of its own, and
+  // waits for dx at its end, before the kernels behind it may start
   if (!a.follows) pdl_wait();
   if (a.leads) pdl_trigger();
   if (warp < kGroupWarps) {
@@ -915,8 +914,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool wide = tl.i0 + rank * kBM + kBM <= a.in;
             auto fetch = [&](int kb) -> int2 {  // a block's 64 row numbers
               const int r = 64 * kb + lane;
-              return make_int2(r < tl.K ? a.rows[tl.row0 + r] : 0,
-                               r + 32 < tl.K ? a.rows[tl.row0 + r + 32] : 0);
+              return make_int2(r < tl.K ? fresh(a.rows + tl.row0 + r) : 0,
+                               r + 32 < tl.K ? fresh(a.rows + tl.row0 + r + 32) : 0);
             };
             int kb = static_cast<int>((mine - no) & (kRowWarps - 1));
             int2 ahead = fetch(kb);

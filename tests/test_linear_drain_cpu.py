@@ -103,3 +103,18 @@ def test_the_kernel_comes_to_every_barrier():
     # then the barriers of the tiles that are left
     assert "walk.at(t)" in rest and "rule.barriers(tl.n, first_c)" in rest
     assert rest.count("half_sync(half)") == 1 and "break" not in rest and "return" not in rest
+
+
+def test_dw_beside_dx_reads_no_array_through_l1():
+    """dW may start without a wait of its own: group arrays and row numbers come from L2."""
+    text = open(os.path.join(libbuild.CSRC, "linear.cuh")).read()
+    table = text[text.index("void build_groups("):]
+    table = table[:table.index("// What the products of one launch read and write")]
+    assert "__ldcg" in text
+    for array in ("off", "ids", "n_groups"):
+        reads = re.findall(rf"\*\s*P\.{array}\b|P\.{array}\[", table)
+        assert not reads and f"fresh(P.{array}" in table
+    text = open(os.path.join(libbuild.CSRC, "linear_tc.cu")).read()
+    grad = text[text.index("if constexpr (C::kGradW) {\n        uint32_t tails"):]
+    grad = grad[:grad.index("} else if (gathers) {")]
+    assert "a.rows[" not in grad and grad.count("fresh(a.rows") == 2
