@@ -47,7 +47,6 @@ namespace {
 
 using namespace tc;
 
-constexpr int kBM = 128;            // i per CTA
 constexpr int kABytes = kBM * 128;  // a k-block's A tile: 128 bytes of k per row
 constexpr int kMaxStages = 12;
 constexpr int kEpiWarps = 8;
@@ -1137,52 +1136,9 @@ cudaError_t launch(const LinearArgs& a, int sms, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-// Which tiles a product takes.  Measured on 16384 rows, 2048 to 4096 wide, a
-// k-block of 128 bytes costs a slot (an SM, or a pair) about
-//   32 wide 305 cycles, 64: 374, 128: 540, pairs of 256: 740;
-// a tile with fewer columns costs in proportion, down to what loading its A
-// and turning a stage over cost.  The estimate is the rounds the slots need
-// times the cost of the tiles; the cheapest is taken.  A
-// batch with many rows per group ends up with pairs of 256 (1550 TFLOP/s
-// against 1090 at 128), a decode batch with 32, and a product with few tiles
-// with narrower ones than its rows would fill, so that more SMs have one
-// (300 rows, 2048 to 512: 40 tiles of 32 in 305 cycles a block against 4
-// pairs in 740).
-struct Shape {
-  int ctas, bn, cycles, least;
-};
-constexpr Shape kShapes[] = {
-    {1, 32, 305, 305}, {1, 64, 374, 330}, {1, 128, 540, 420}, {2, 256, 740, 480}};
-
-int64_t round_cost(const Shape& sh, int64_t I, int64_t rows, int64_t live, int sms) {
-  const int64_t each = (rows + live - 1) / live;
-  // the tiles of one group exactly; of many, half a tile more for each group's end
-  int64_t per = live == 1 ? (rows + sh.bn - 1) / sh.bn : (2 * rows / sh.bn + live) / 2;
-  if (per < live) per = live;
-  // groups are uneven: where the mean one fills half a tile, some fill all of it
-  int64_t cost = sh.cycles;
-  if (2 * each < sh.bn) {
-    cost = sh.cycles * each / sh.bn;
-    if (cost < sh.least) cost = sh.least;
-  }
-  const int64_t tiles = per * ((I + kBM * sh.ctas - 1) / (kBM * sh.ctas)), slots = sms / sh.ctas;
-  return (tiles + slots - 1) / slots * cost;
-}
-
 template <Product P, bool F32>
 cudaError_t pick(const LinearArgs& a, int sms, cudaStream_t s) {
-  const int64_t live = a.g.G < a.g.M ? a.g.G : a.g.M;
-  int best = 0;
-  int64_t least = 0;
-  for (int q = 0; q < 4; ++q) {
-    const int64_t c =
-        round_cost(kShapes[q], P == Product::kGradX ? a.in : a.out, a.g.M, live, sms);
-    if (q == 0 || c < least) {
-      best = q;
-      least = c;
-    }
-  }
-  switch (best) {
+  switch (pick_shape(P == Product::kGradX ? a.in : a.out, a.g.M, a.g.G, sms)) {
     case 0: return launch<P, 1, 32, F32>(a, sms, s);
     case 1: return launch<P, 1, 64, F32>(a, sms, s);
     case 2: return launch<P, 1, 128, F32>(a, sms, s);
@@ -1190,19 +1146,10 @@ cudaError_t pick(const LinearArgs& a, int sms, cudaStream_t s) {
   }
 }
 
-// dW: pairs of 256 x 256, or single CTAs of 128 x 128 where those leave a
-// third or more of a pair's columns idle or give the SMs fewer rounds.  A tile
-// costs its products (740 or 540 cycles per 64 rows) or its way out (4500 or
-// 2300), whichever is more.
 cudaError_t pick_grad_w(const LinearArgs& a, int sms, cudaStream_t s) {
-  const int64_t blocks = (a.g.M / a.g.G + 63) / 64;
-  auto cost = [&](int64_t m, int64_t n, int64_t slots, int64_t block, int64_t out) {
-    const int64_t tiles = (a.in + m - 1) / m * ((a.out + n - 1) / n) * a.g.G;
-    return (tiles + slots - 1) / slots * (blocks * block > out ? blocks * block : out);
-  };
-  const bool pairs = cost(256, 256, sms / 2, 740, 4500) <= cost(128, 128, sms, 540, 2300);
-  return pairs ? launch<Product::kGradW, 2, 256, true>(a, sms, s)
-               : launch<Product::kGradW, 1, 128, true>(a, sms, s);
+  return grad_w_pairs(a.in, a.out, a.g.M, a.g.G, sms)
+             ? launch<Product::kGradW, 2, 256, true>(a, sms, s)
+             : launch<Product::kGradW, 1, 128, true>(a, sms, s);
 }
 
 }  // namespace

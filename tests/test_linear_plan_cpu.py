@@ -8,6 +8,7 @@ import numpy as np
 import pytest
 
 from atomic_expert_routing_b200 import build as libbuild
+from linear_cases import GRAD_W, GRAD_W_IDS, ROW_IDS, ROWS
 
 SHIM = r"""
 #include "linear_plan.h"
@@ -25,6 +26,10 @@ void wait_limits(int n, const int32_t* blocks, const uint8_t* tail, uint32_t* li
     }
   }
 }
+int shape(int64_t I, int64_t rows, int64_t G, int sms) { return pick_shape(I, rows, G, sms); }
+int pairs(int64_t in, int64_t out, int64_t rows, int64_t G, int sms) {
+  return grad_w_pairs(in, out, rows, G, sms);
+}
 }
 """
 
@@ -36,7 +41,10 @@ def plan(tmp_path_factory):
     src.write_text(SHIM)
     subprocess.run(["g++", "-std=c++17", "-O1", "-shared", "-fPIC", "-Wall", "-Werror", "-I",
                     libbuild.CSRC, "-o", str(so), str(src)], check=True)
-    return C.CDLL(str(so))
+    lib = C.CDLL(str(so))
+    lib.shape.argtypes = [C.c_int64] * 3 + [C.c_int]
+    lib.pairs.argtypes = [C.c_int64] * 4 + [C.c_int]
+    return lib
 
 
 # what a block of 64 rows and a tile's way out take at most, in seconds: a CTA's share of the
@@ -80,3 +88,35 @@ def test_a_wait_for_rows_to_zero_outlasts_what_the_cta_sums_before(plan, name):
         assert (limits[at] <= 2 + 10 * lasts).all()
         waits += len(at)
     assert waits
+
+
+# ---- which kernel a product takes -----------------------------------------------------
+
+SMS, WIDTHS = 148, (32, 64, 128, 256)
+
+
+@pytest.mark.parametrize("width,several,sizes,I,K", ROWS, ids=ROW_IDS)
+def test_rows_cases_reach_their_kernel(plan, width, several, sizes, I, K):
+    assert WIDTHS[plan.shape(I, sum(sizes), len(sizes), SMS)] == width
+    pair = 2 if width == 256 else 1
+    tiles = sum(-(-r // width) for r in sizes) * -(-I // (128 * pair))
+    assert (tiles > SMS // pair) == several
+    assert any(r % 32 for r in sizes) and K % 64  # ends inside a tile and inside a k-block
+
+
+@pytest.mark.parametrize("pairs,several,sizes,n_in,n_out", GRAD_W, ids=GRAD_W_IDS)
+def test_grad_w_cases_reach_their_kernel(plan, pairs, several, sizes, n_in, n_out):
+    assert bool(plan.pairs(n_in, n_out, sum(sizes), len(sizes), SMS)) == pairs
+    m = 256 if pairs else 128
+    tiles = -(-n_in // m) * -(-n_out // m) * len(sizes)
+    assert (tiles > SMS // (2 if pairs else 1)) == several
+    assert any(r % 16 for r in sizes)  # with rows to zero
+
+
+def test_every_kernel_has_cases():
+    assert {w for w, *_ in ROWS} == set(WIDTHS) and {p for p, *_ in GRAD_W} == {False, True}
+    for w in WIDTHS:
+        assert {s for v, s, *_ in ROWS if v == w} == {False, True}
+    for p in (False, True):
+        assert {s for v, s, *_ in GRAD_W if v == p} == {False, True}
+    assert any(k > 512 for *_, k in ROWS)
