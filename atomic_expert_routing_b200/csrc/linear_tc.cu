@@ -48,7 +48,7 @@ namespace {
 using namespace tc;
 
 constexpr int kABytes = kBM * 128;  // a k-block's A tile: 128 bytes of k per row
-constexpr int kMaxStages = 12;
+constexpr int kMaxStages = 6;
 constexpr int kEpiWarps = 8;
 constexpr int kLoadWarp = kEpiWarps, kMmaWarp = kEpiWarps + 1, kLoadWarpB = kEpiWarps + 2;
 constexpr int kRowWarp = kEpiWarps + 4;
@@ -359,6 +359,7 @@ struct Cfg {
   static_assert((kSmemLimit - 600 - 1024 - kOut - OMNI_MAX_GROUPS * sizeof(GroupTab)) / kStage >=
                     kRowWarps,
                 "the row warps' turns need as many stages");
+  static_assert((kSmemLimit - 1024 - kOut) / kStage <= kMaxStages, "a barrier for each stage");
   static_assert(!kGradW || kNb % 64 == 0, "dW's B tile is made of 64-wide boxes");
 };
 
@@ -1097,8 +1098,7 @@ cudaError_t launch(const LinearArgs& a, int sms, cudaStream_t s) {
   if (!ok) return cudaErrorInvalidValue;
   const size_t fixed = 1024 + C::kOut + sizeof(GroupTab) * static_cast<size_t>(a.g.G);
   const size_t statics = sizeof(GroupScratch) + (3 * kMaxStages + 5) * 8 + 64;
-  int stages = static_cast<int>((kSmemLimit - statics - fixed) / C::kStage);
-  if (stages > kMaxStages) stages = kMaxStages;
+  const int stages = static_cast<int>((kSmemLimit - statics - fixed) / C::kStage);
   const size_t smem = fixed + static_cast<size_t>(stages) * C::kStage;
   auto kernel = k_linear_tc<P, CTAS, BN, F32>;
   int dev = 0;

@@ -193,8 +193,11 @@ cudaError_t launch(int64_t n, int width, const void* src, int8_t* q, float* scal
     const unsigned grid = static_cast<unsigned>((n + rows_per_cta - 1) / rows_per_cta);
     return launch_k(kernel, grid, kThreads, 0, s, n, width, p, q, scale);
   };
+  int dev = 0, sms = 148;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   // two warps per row once that gives every SM a few CTAs
-  if (width <= 64 * 8 * 4 && n >= 148 * 4 * (kThreads / 64))
+  if (width <= 64 * 8 * 4 && n >= int64_t(4) * sms * (kThreads / 64))
     OMNI_TRY(go(k_quantize_rows<T, 64, 4>, kThreads / 64));
   else if (width <= kThreads * 8 * 8)
     OMNI_TRY(go(k_quantize_rows<T, kThreads, 8>, 1));
