@@ -190,13 +190,15 @@ class Workspace:
         if self.buf is None or self.buf.numel() < nbytes or self.buf.device != device:
             self.buf = _new(torch.empty, stream, device, torch.uint8, nbytes)
             self._users = set()
-        if self.buf.device.type == "cpu":
+        if self.buf.is_cpu:
             return self.buf  # refused by the call
-        on = torch.cuda.current_stream(device) if stream is None else stream
-        if on.cuda_stream not in self._users:
+        on = torch._C._cuda_getCurrentRawStream(self.buf.get_device()) if stream is None \
+            else stream.cuda_stream
+        if on not in self._users:
             # it may be another stream's memory, and be let go while this call runs
-            self.buf.record_stream(_torch_stream(on, device))
-            self._users.add(on.cuda_stream)
+            self.buf.record_stream(torch.cuda.current_stream(device) if stream is None
+                                   else _torch_stream(stream, device))
+            self._users.add(on)
         return self.buf
 
 
@@ -660,6 +662,8 @@ def _linear_out(name, t, like, M, width, dtype, stream):
     tensor of dtype beside like; and its dtype's code."""
     if t is None:
         code = _out_code("out_dtype", dtype)
+        if stream is None:
+            return torch.empty(M, width, dtype=dtype, device=like.device), code
         return _new(torch.empty, stream, like.device, dtype, M, width), code
     code = _out_code(name, t.dtype)
     _expect_rows(name, t, M, (width,), t.dtype)
@@ -702,7 +706,8 @@ def grouped_linear_backward(x, W, dy, group_off, *, ids=None, n_groups=None, row
     sizes = _linear_sizes(_BACKWARD_ARGS, x, W, group_off, ids, n_groups, rows, counts,
                           torch.bfloat16)
     M, _, n_in, n_out, E, G = sizes
-    _expect_rows("dy", dy, M, (n_out,), torch.bfloat16)
+    if dy.shape != (M, n_out) or dy.dtype != torch.bfloat16:
+        _expect_rows("dy", dy, M, (n_out,), torch.bfloat16)
     if not (need_dx or need_dW):
         raise ValueError("need_dx and need_dW: no gradient asked for")
     g, code = {}, OMNI_BF16
@@ -712,7 +717,8 @@ def grouped_linear_backward(x, W, dy, group_off, *, ids=None, n_groups=None, row
         if dW is None:
             # with ids or n_groups some matrices may be in no group
             make = torch.empty if ids is None and n_groups is None and G == E else torch.zeros
-            g["dW"] = _new(make, stream, W.device, torch.float32, E, n_out, n_in)
+            g["dW"] = make(E, n_out, n_in, dtype=torch.float32, device=W.device) \
+                if stream is None else _new(make, stream, W.device, torch.float32, E, n_out, n_in)
             accumulate = False
         else:
             _expect_rows("dW", dW, E, (n_out, n_in), torch.float32)
@@ -739,11 +745,14 @@ def quantize_rows(x, *, q=None, scale=None, stream=None):
     width = shape[-1]
     n = x.numel() // max(width, 1)
     if q is None:
-        q = _new(torch.empty, stream, x.device, torch.int8, *shape)
+        q = torch.empty(*shape, dtype=torch.int8, device=x.device) if stream is None \
+            else _new(torch.empty, stream, x.device, torch.int8, *shape)
     else:
         _expect_rows("q", q, n, (width,), torch.int8)
     if scale is None:
-        scale = _new(torch.empty, stream, x.device, torch.float32, *shape[:-1])
+        scale = torch.empty(*shape[:-1], dtype=torch.float32, device=x.device) \
+            if stream is None and len(shape) > 1 \
+            else _new(torch.empty, stream, x.device, torch.float32, *shape[:-1])
     else:
         _expect("scale", scale, n, torch.float32)
     index = _index(x)
@@ -769,7 +778,9 @@ def quantized_linear(xq, xs, Wq, Ws, group_off=None, *, ids=None, n_groups=None,
                           torch.int8)
     M, T, _, n_out, E, _ = sizes
     _expect("xs", xs, T, torch.float32)
-    _expect_rows("Ws", Ws, E, (n_out,), torch.float32)
+    _expect("Ws", Ws, E * n_out, torch.float32)
+    if Ws.dim() > 1 and Ws.shape != (E, n_out):
+        _expect_rows("Ws", Ws, E, (n_out,), torch.float32)
     y, code = _linear_out("y", y, xq, M, n_out, out_dtype, stream)
     index = _index(xq)
     _run("omni_quantized_linear", index, stream,

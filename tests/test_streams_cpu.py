@@ -38,6 +38,8 @@ def made(monkeypatch):
         monkeypatch.setattr(torch, name, recorded(name))
     monkeypatch.setattr(torch.cuda, "stream", on)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: HERE)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: HERE.cuda_stream,
+                        raising=False)
     monkeypatch.setattr(torch.cuda, "ExternalStream",
                         lambda ptr, device=None: SimpleNamespace(cuda_stream=ptr))
     monkeypatch.setattr(torch.Tensor, "record_stream",
