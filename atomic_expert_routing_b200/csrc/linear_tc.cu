@@ -27,15 +27,18 @@
 // Pieces: the tensor core's fp32 sums cut every addition towards zero, an
 // error of about 1.1e-9 of the result per term of k.  bf16 results do not
 // show it; fp32 results are summed in pieces of 512 terms, which the draining
-// warps add up in registers, rounded to nearest.
+// warps add up in registers, rounded to nearest.  Within a piece the cuts
+// remain, all one way: 3e-7 to 5e-7 from 64 bits, about twice what fp32 sums
+// rounded to nearest are off by (1.2e-7 to 2.5e-7).
 //
 // Bounds and measurements (kernel times on one B200, short bursts).  Long
 // groups: the tensor pipe; 16384 rows, 2048 to 4096: forward 172-180 us (1530
-// to 1600 TFLOP/s of a measured 1673), gathered 189, dx 178, 8-bit 94-100
-// (2750 to 2930 TOP/s).  Decode: HBM; 512 rows on 64 experts of 2048 to 1024
-// read 268 MB in 46 us (5.8 TB/s).  dW of short groups: its own writes; 64
-// matrices of 4096 x 2048 in fp32 take 403 us for 16 rows each (5.3 TB/s),
-// 435 for 256.  Single tokens: latency, 5 us for the smallest call.
+// to 1600 TFLOP/s of a measured 1673), gathered 187-190, dx 175-180, 8-bit
+// 90-100 (2750 to 3060 TOP/s).  Decode: HBM; 512 rows on 64 experts of 2048 to
+// 1024 read 268 MB in 46 us (5.8 TB/s).  dW of short groups: its own writes;
+// 64 matrices of 4096 x 2048 in fp32 take 391-403 us for 16 rows each (5.3 to
+// 5.5 TB/s), 425-440 for 256.  Single tokens: latency, 5 us for the smallest
+// call.
 #include <atomic>
 
 #include "linear.cuh"
@@ -124,12 +127,13 @@ __device__ __forceinline__ void copy16_or_zero(uint32_t dst, const void* src, bo
 __device__ __forceinline__ void copies_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
-// Arrive on an mbarrier of either CTA of a pair.  What the arrival reports has
-// been observed by this thread (a completed barrier phase, a fence, a finished
-// TMEM load), and lies in this CTA's shared memory or TMEM, where the tensor
-// core reads or writes it in place; the arrival need not push this thread's
-// writes out to the cluster (.release.cluster: some 2000 cycles each, 558
-// against 206 us for dW of 16384 x 2048 x 4096 with one per stage).
+// Arrive on an mbarrier of either CTA of a pair, without a release at cluster
+// scope.  What the arrival reports has been observed by this thread (a
+// completed barrier phase, a fence, a finished TMEM load), and lies in this
+// CTA's shared memory or TMEM, where the tensor core reads or writes it in
+// place.  That the other CTA's products see it is an assumption: PTX promises
+// it for an arrival with .release.cluster only, which costs some 2000 cycles
+// (558 against 206 us for dW of 16384 x 2048 x 4096 with one per stage).
 __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }

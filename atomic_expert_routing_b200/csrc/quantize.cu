@@ -5,8 +5,10 @@
 // by a CTA of eight (up to 16384 values; a decode batch's few rows would leave
 // most of the GPU idle with a warp each); longer rows are read twice.
 //
-// Bound by its instructions (56% of the issue slots): 16384 x 2048 bf16 take
-// 28 us (15 at the copy rate), the same in fp32 27 us (6.2 TB/s), 64 rows 2.7.
+// 16384 x 2048 in fp32 take 27 us, at the memory's rate (6.2 TB/s); in bf16,
+// half the bytes read, 28 (15 at the copy rate; 2.4 TB/s and 54% of the issue
+// slots, so neither of the two bounds it, and what does was not found); 64
+// rows 2.7.
 //
 // The quotient is rounded exactly, as if formed in infinite precision: the
 // fp32 quotient can land on the middle between two integers when the true

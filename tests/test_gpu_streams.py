@@ -125,3 +125,31 @@ def test_schedule_and_backward_behind_a_busy_stream():
         # is taken as up to twice the largest result
         tol = 2 * (2.0 ** -7 + 256 * 2.0 ** -23) * float(a.abs().max())
         assert bool(a.any()) and float((a - g1[k]).abs().max()) <= tol
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_a_stream_forked_inside_a_capture(name):
+    """A call on a second stream of a capture: its outputs and fills are part of the graph, and
+    replays give the same again."""
+    call = _case()[name]
+    ref = call(None)
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    with torch.cuda.stream(main):
+        call(None)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=main):
+        side.wait_stream(main)
+        first = call(side)
+        call(side)  # outputs that nobody keeps
+        got = call(side)
+        main.wait_stream(side)
+    for _ in range(2):
+        for t in got + first:
+            t.fill_(9)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for out in (first, got):
+            assert all(torch.equal(a, b) for a, b in zip(out, ref))
+    del graph
